@@ -356,6 +356,105 @@ int plx_decode_fp8kv(const void* q, const void* r, const void* Kcodes, const flo
                      int H, int Hkv, int L, int d, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Writes 4-bit KV cache rows: a row x of d bf16 values (d in {64, 128}) becomes
+ * d codes of four bits (codes [rows, d/2], element 2i in the low half of byte i)
+ * and a pair of bf16 numbers (params [rows, 2]), a scale s and a zero point z:
+ *   lo = min(0, min x), hi = max(0, max x)
+ *   s = the smallest bf16 value >= (hi - lo) / 15,  z = rint(-lo / s)
+ *   c = min(15, rint(x / s) + z)          (nearest integer, ties to even)
+ * and stands for s (c - z), at most s / 2 away.  Zero is held exactly; an
+ * all-zero row has s = z = 0; a row that holds an infinity or a NaN has s = NaN
+ * and stands for NaN.  d/2 + 4 bytes a row where bf16 takes 2 d.  The pages name
+ * fp8 (rainbus.top summary, reproduction notes); four bits are this build's
+ * extension of that cache.  X and codes 16-byte aligned, params 4-byte aligned,
+ * else PLX_ERR_MISALIGNED; rows >= 1.
+ */
+int plx_kv_quantize_int4(const void* X, void* codes, void* params, long long rows, int d, void* stream);
+
+/* The bf16 values (out [rows, d], s (c - z) rounded once) of 4-bit rows. */
+int plx_kv_dequantize_int4(const void* codes, const void* params, void* out, long long rows, int d, void* stream);
+
+/*
+ * Appends one decode step's rows to a 4-bit cache: the key and value rows k, v
+ * (bf16 [B, Hkv, d]) of sequence b go to row seqlens[b] - 1 of Kcodes, Vcodes
+ * [B, Hkv, L, d/2] and Kparams, Vparams [B, Hkv, L, 2], as plx_kv_quantize_int4
+ * writes them.  k_out, v_out (bf16 [B, Hkv, d], each may be NULL) get the values
+ * the rows now stand for.  A seqlens entry outside 1..L writes no row, zeros its
+ * k_out and v_out and reports PLX_ERR_BAD_SEQLEN.
+ */
+int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams, void* Vcodes, void* Vparams,
+                       const int32_t* seqlens, void* k_out, void* v_out, int B, int Hkv, int L, int d,
+                       void* stream);
+
+/*
+ * One decode step over a 4-bit KV cache (plx_kv_quantize_int4 / _append_int4):
+ * the result of plx_decode_gqa over the cache values s (c - z), which are not
+ * rounded to bf16 (rainbus.top summary, 方法步骤详情: the streamed S1/S2, O1/O2
+ * form).  q, r, out: bf16 [B, H, d]; codes uint8 [B, Hkv, L, d/2]; params bf16
+ * [B, Hkv, L, 2]; seqlens int32 [B] in 1..L (others write zeros and report
+ * PLX_ERR_BAD_SEQLEN).  Query head h reads KV head h / (H/Hkv), groups of 1, 2, 4
+ * or 8; d in {64, 128}, else PLX_ERR_UNSUPPORTED.  Cache rows at and behind
+ * seqlens[b] are not read.  It reads 2 (d/2 + 4) bytes a cached key.
+ * workspace: plx_decode_int4kv_workspace_bytes() bytes, 256-byte aligned, no
+ * initial contents; NULL is allowed where that is 0, else PLX_ERR_WORKSPACE.
+ * Nothing else is shared between calls: calls with different workspaces may run
+ * at the same time.  Codes 16-byte, params and seqlens 4-byte aligned.
+ */
+size_t plx_decode_int4kv_workspace_bytes(int B, int H, int Hkv, int L, int d);
+int plx_decode_int4kv(const void* q, const void* r, const void* Kcodes, const void* Kparams, const void* Vcodes,
+                      const void* Vparams, const int32_t* seqlens, void* out, int B, int H, int Hkv, int L, int d,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode steps that also collect attention weight: out as plx_decode_gqa (bf16
+ * cache) or plx_decode_int4kv (4-bit cache), and for every visible key j
+ *   weights_out[b,g,j] = weights[b,g,j] + sum over the heads h of KV head g of p_hj,
+ * p the softmax weights (rainbus.top summary, "Softmax Attention"), all fp32
+ * [B, Hkv, L].  weights_out may be weights (running totals over the steps), any
+ * other overlap gives PLX_ERR_INVALID_ARG; its entries at and behind seqlens[b], and those of a sequence whose seqlens entry
+ * is outside 1..L, are left as they were.  A new key's entry has to be 0 before
+ * its first step.  bf16 caches [B, Hkv, L, d].  workspace:
+ * plx_decode_weights_workspace_bytes() bytes (partial records and one fp32 score
+ * for each query head and key), 256-byte aligned, no initial contents, required
+ * (else PLX_ERR_WORKSPACE).  Sizes, alignment and independence of calls as
+ * plx_decode_int4kv.
+ */
+size_t plx_decode_weights_workspace_bytes(int B, int H, int Hkv, int L, int d);
+int plx_decode_weights(const void* q, const void* r, const void* Kcache, const void* Vcache,
+                       const int32_t* seqlens, const float* weights, float* weights_out, void* out, int B, int H,
+                       int Hkv, int L, int d, void* workspace, size_t workspace_bytes, void* stream);
+int plx_decode_int4kv_weights(const void* q, const void* r, const void* Kcodes, const void* Kparams,
+                              const void* Vcodes, const void* Vparams, const int32_t* seqlens,
+                              const float* weights, float* weights_out, void* out, int B, int H, int Hkv, int L,
+                              int d, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Thins KV caches out by collected attention weight.  Every sequence with
+ * seqlens[b] > budget keeps, for each KV head on its own, its first `sinks` rows,
+ * its last `recent` rows and the budget - sinks - recent rows between them with
+ * the largest weights (ties: the lower index stays; a NaN weight ranks below
+ * every number); shorter sequences keep all rows.  Kept rows move to the front,
+ * in the order of their positions:
+ *   kept[b,g,i]        = position of kept row i (int32 [B, Hkv, min(budget, L)], -1 behind the last)
+ *   caches_out[c][b,g,i] = caches[c][b,g,kept[b,g,i]]   (rows behind the last are left as they were)
+ *   weights_out[b,g,i] = weights[b,g,kept[b,g,i]]       (fp32 [B, Hkv, L_out], 0 behind the last)
+ *   seqlens_out[b]     = min(seqlens[b], budget)
+ * caches: HOST arrays of `count` (0..8) device pointers to tensors [B, Hkv, L]
+ * of rows of row_bytes[c] (1..65536) bytes: bf16, fp32, e4m3 or 4-bit rows, their
+ * scales or params; caches_out [B, Hkv, L_out], L_out >= min(budget, L).  In
+ * place: caches_out[c] = caches[c] or weights_out = weights, with L_out = L;
+ * seqlens_out may be seqlens.  Other overlaps of an output with a cache, the
+ * weights or another output give PLX_ERR_INVALID_ARG, as do
+ * budget < 1, negative sinks or recent, and sinks + recent > budget.  A seqlens
+ * entry outside 1..L keeps nothing (kept -1, weights_out 0, length 0, rows
+ * untouched) and reports PLX_ERR_BAD_SEQLEN.  Two launches; no workspace.
+ */
+int plx_cache_evict(int count, const void* const* caches, void* const* caches_out, const int* row_bytes,
+                    const float* weights, float* weights_out, const int32_t* seqlens, int32_t* seqlens_out,
+                    int32_t* kept, int B, int Hkv, int L, int L_out, int budget, int sinks, int recent,
+                    void* stream);
+
+/*
  * plx_decode_noalloc — one bf16 decode step that allocates nothing.
  * (The paper has no counterpart: this is a deployment variant of plx_decode_ex.)
  *

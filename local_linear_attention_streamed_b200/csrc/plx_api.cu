@@ -67,6 +67,7 @@ int current_device(DeviceCache** out) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The CUDA error behind this thread's last PLX_ERR_CUDA from a launch
 // (plx_last_cuda_error reports it).
@@ -626,6 +627,194 @@ int plx_decode_fp8kv(const void* q, const void* r, const void* Kcodes, const flo
     }
   }
   return cuda_rc(launch_decode_fp8kv(a, st, dc->num_sms));
+}
+
+int plx_kv_quantize_int4(const void* X, void* codes, void* params, long long rows, int d, void* stream) {
+  if (!X || !codes || !params || rows < 1) return PLX_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
+  if (!aligned16(X) || !aligned16(codes) || !aligned4(params)) return PLX_ERR_MISALIGNED;
+  DeviceCache* dc = nullptr;
+  int rc = current_device(&dc);
+  if (rc != PLX_OK) return rc;
+  return cuda_rc(
+      launch_kv_quantize_int4(X, codes, params, rows, d, reinterpret_cast<cudaStream_t>(stream), dc->num_sms));
+}
+
+int plx_kv_dequantize_int4(const void* codes, const void* params, void* out, long long rows, int d, void* stream) {
+  if (!codes || !params || !out || rows < 1) return PLX_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
+  if (!aligned16(out) || !aligned16(codes) || !aligned4(params)) return PLX_ERR_MISALIGNED;
+  DeviceCache* dc = nullptr;
+  int rc = current_device(&dc);
+  if (rc != PLX_OK) return rc;
+  return cuda_rc(
+      launch_kv_dequantize_int4(codes, params, out, rows, d, reinterpret_cast<cudaStream_t>(stream), dc->num_sms));
+}
+
+int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams, void* Vcodes, void* Vparams,
+                       const int32_t* seqlens, void* k_out, void* v_out, int B, int Hkv, int L, int d,
+                       void* stream) {
+  if (!k || !v || !Kcodes || !Kparams || !Vcodes || !Vparams || !seqlens) return PLX_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || L < 1 || d < 1) return PLX_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(Kcodes) || !aligned16(Vcodes) || !aligned16(k_out) ||
+      !aligned16(v_out) || !aligned4(Kparams) || !aligned4(Vparams) || !aligned4(seqlens))
+    return PLX_ERR_MISALIGNED;
+  if (!decode_sizes_supported(B, Hkv, Hkv, L)) return PLX_ERR_UNSUPPORTED;
+  DeviceCache* dc = nullptr;
+  int rc = current_device(&dc);
+  if (rc != PLX_OK) return rc;
+  Int4AppendArgs a{k, v, Kcodes, Kparams, Vcodes, Vparams, seqlens, k_out, v_out, B, Hkv, L, d, dc->status};
+  return cuda_rc(launch_kv_append_int4(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static size_t cache_decode_bytes(int B, int H, int Hkv, int L, int d, bool weights) {
+  if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0) return 0;
+  const CacheDecodeSpace w = cache_decode_space(B, H, Hkv, L, d, num_sms_or_default(), weights);
+  return w.partials + w.scores;
+}
+
+size_t plx_decode_int4kv_workspace_bytes(int B, int H, int Hkv, int L, int d) {
+  return cache_decode_bytes(B, H, Hkv, L, d, false);
+}
+
+size_t plx_decode_weights_workspace_bytes(int B, int H, int Hkv, int L, int d) {
+  return cache_decode_bytes(B, H, Hkv, L, d, true);
+}
+
+static int cache_decode_impl(const void* q, const void* r, const void* K, const void* Kp, const void* V,
+                             const void* Vp, bool int4, const int32_t* seqlens, const float* w_in, float* w_out,
+                             bool weights, void* out, int B, int H, int Hkv, int L, int d, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!q || !r || !K || !V || !seqlens || !out || (int4 && (!Kp || !Vp)) || (weights && (!w_in || !w_out)))
+    return PLX_ERR_INVALID_ARG;
+  if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0) return PLX_ERR_INVALID_ARG;
+  const int G = H / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return PLX_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(r) || !aligned16(K) || !aligned16(V) || !aligned16(out) || !aligned4(seqlens) ||
+      !aligned4(Kp) || !aligned4(Vp) || !aligned4(w_in) || !aligned4(w_out))
+    return PLX_ERR_MISALIGNED;
+  if (!decode_sizes_supported(B, H, Hkv, L)) return PLX_ERR_UNSUPPORTED;
+  if (weights && w_in != w_out) {  // the same array or apart
+    const uintptr_t w0 = reinterpret_cast<uintptr_t>(w_in), w1 = reinterpret_cast<uintptr_t>(w_out);
+    const size_t bytes = 4 * (size_t)B * Hkv * L;
+    if (w0 < w1 + bytes && w1 < w0 + bytes) return PLX_ERR_INVALID_ARG;
+  }
+  DeviceCache* dc = nullptr;
+  int rc = current_device(&dc);
+  if (rc != PLX_OK) return rc;
+  const CacheDecodeSpace need = cache_decode_space(B, H, Hkv, L, d, dc->num_sms, weights);
+  if (need.partials + need.scores > 0) {
+    if (!workspace || workspace_bytes < need.partials + need.scores) return PLX_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PLX_ERR_MISALIGNED;
+  }
+  CacheDecodeArgs a{};
+  a.q = q;
+  a.r = r;
+  a.K = K;
+  a.V = V;
+  a.Kp = int4 ? Kp : nullptr;
+  a.Vp = int4 ? Vp : nullptr;
+  a.seqlens = seqlens;
+  a.out = out;
+  a.w_in = w_in;
+  a.w_out = weights ? w_out : nullptr;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.d = d;
+  a.splits = need.splits;
+  a.partials = need.partials ? static_cast<float*>(workspace) : nullptr;
+  a.scores = need.scores ? reinterpret_cast<float*>(static_cast<char*>(workspace) + need.partials) : nullptr;
+  a.status = dc->status;
+  return cuda_rc(launch_cache_decode(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int plx_decode_int4kv(const void* q, const void* r, const void* Kcodes, const void* Kparams, const void* Vcodes,
+                      const void* Vparams, const int32_t* seqlens, void* out, int B, int H, int Hkv, int L, int d,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  return cache_decode_impl(q, r, Kcodes, Kparams, Vcodes, Vparams, true, seqlens, nullptr, nullptr, false, out, B, H,
+                           Hkv, L, d, workspace, workspace_bytes, stream);
+}
+
+int plx_decode_int4kv_weights(const void* q, const void* r, const void* Kcodes, const void* Kparams,
+                              const void* Vcodes, const void* Vparams, const int32_t* seqlens, const float* weights,
+                              float* weights_out, void* out, int B, int H, int Hkv, int L, int d, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  return cache_decode_impl(q, r, Kcodes, Kparams, Vcodes, Vparams, true, seqlens, weights, weights_out, true, out, B,
+                           H, Hkv, L, d, workspace, workspace_bytes, stream);
+}
+
+int plx_decode_weights(const void* q, const void* r, const void* Kcache, const void* Vcache, const int32_t* seqlens,
+                       const float* weights, float* weights_out, void* out, int B, int H, int Hkv, int L, int d,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  return cache_decode_impl(q, r, Kcache, nullptr, Vcache, nullptr, false, seqlens, weights, weights_out, true, out, B,
+                           H, Hkv, L, d, workspace, workspace_bytes, stream);
+}
+
+int plx_cache_evict(int count, const void* const* caches, void* const* caches_out, const int* row_bytes,
+                    const float* weights, float* weights_out, const int32_t* seqlens, int32_t* seqlens_out,
+                    int32_t* kept, int B, int Hkv, int L, int L_out, int budget, int sinks, int recent,
+                    void* stream) {
+  if (count < 0 || (count > 0 && (!caches || !caches_out || !row_bytes)) || !weights || !weights_out || !seqlens ||
+      !seqlens_out || !kept)
+    return PLX_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || L < 1 || budget < 1 || sinks < 0 || recent < 0 || (long long)sinks + recent > budget ||
+      L_out < std::min(budget, L))
+    return PLX_ERR_INVALID_ARG;
+  if (count > kEvictMaxCaches) return PLX_ERR_UNSUPPORTED;
+  if (!decode_sizes_supported(B, Hkv, Hkv, L) || !decode_sizes_supported(B, Hkv, Hkv, L_out))
+    return PLX_ERR_UNSUPPORTED;
+  EvictArgs a{};
+  a.count = count;
+  const long long units = (long long)B * Hkv;
+  uintptr_t span[kEvictMaxCaches + 1][4];  // [source, end, destination, end] of the caches so far
+  for (int c = 0; c <= count; ++c) {
+    const bool totals = c == count;
+    const void* s = totals ? weights : caches[c];
+    void* t = totals ? weights_out : caches_out[c];
+    const int rb = totals ? 4 : row_bytes[c];
+    if (!s || !t || rb < 1) return PLX_ERR_INVALID_ARG;
+    if (rb > 65536) return PLX_ERR_UNSUPPORTED;
+    // In place is the same address and capacity; any other overlap of what is
+    // written with what is read or written is refused.
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(s), t0 = reinterpret_cast<uintptr_t>(t);
+    const uintptr_t s1 = s0 + (size_t)units * L * rb, t1 = t0 + (size_t)units * L_out * rb;
+    if (s0 == t0 ? L_out != L : s0 < t1 && t0 < s1) return PLX_ERR_INVALID_ARG;
+    for (int o = 0; o < c; ++o) {
+      if ((span[o][0] < t1 && t0 < span[o][1]) || (span[o][2] < t1 && t0 < span[o][3]) ||
+          (s0 < span[o][3] && span[o][2] < s1))
+        return PLX_ERR_INVALID_ARG;
+    }
+    span[c][0] = s0, span[c][1] = s1, span[c][2] = t0, span[c][3] = t1;
+    if (!totals) {
+      a.src[c] = s;
+      a.dst[c] = t;
+      a.row_bytes[c] = rb;
+    }
+  }
+  if (!aligned4(weights) || !aligned4(weights_out) || !aligned4(seqlens) || !aligned4(seqlens_out) ||
+      !aligned4(kept))
+    return PLX_ERR_MISALIGNED;
+  DeviceCache* dc = nullptr;
+  int rc = current_device(&dc);
+  if (rc != PLX_OK) return rc;
+  a.w = weights;
+  a.w_out = weights_out;
+  a.seqlens = seqlens;
+  a.seqlens_out = seqlens_out;
+  a.kept = kept;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.L = L;
+  a.Lout = L_out;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.status = dc->status;
+  return cuda_rc(launch_cache_evict(a, reinterpret_cast<cudaStream_t>(stream), dc->num_sms));
 }
 
 size_t plx_decode_window_workspace_bytes(int B, int H, int Hkv, int L, int d, int window) {

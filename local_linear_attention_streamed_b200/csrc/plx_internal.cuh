@@ -193,6 +193,70 @@ cudaError_t launch_qkr_norm_rope(const void* x, void* y, int B, int N, int H, in
 cudaError_t launch_swap_axes(const void* src, void* dst, int B, int A1, int A2, int d,
                              cudaStream_t st);
 
+// 4-bit cache rows (kv_int4.cu): codes [rows, d/2] and one 32-bit word a row,
+// bf16 scale in the low half and bf16 zero point in the high half.
+cudaError_t launch_kv_quantize_int4(const void* X, void* codes, void* params, long long rows, int d,
+                                    cudaStream_t st, int num_sms);
+cudaError_t launch_kv_dequantize_int4(const void* codes, const void* params, void* out, long long rows, int d,
+                                      cudaStream_t st, int num_sms);
+struct Int4AppendArgs {
+  const void* k;  // bf16 [B, Hkv, d]
+  const void* v;
+  void* Kcodes;  // [B, Hkv, L, d/2]
+  void* Kparams;
+  void* Vcodes;
+  void* Vparams;
+  const int32_t* seqlens;
+  void* k_out;  // bf16 [B, Hkv, d] or null
+  void* v_out;
+  int B, Hkv, L, d;
+  int* status;
+};
+cudaError_t launch_kv_append_int4(const Int4AppendArgs& a, cudaStream_t st);
+
+// Decode over a 4-bit cache, and decodes that collect softmax weights
+// (decode_cache.cu).
+struct CacheDecodeArgs {
+  const void* q;
+  const void* r;
+  const void* K;  // codes (Kp set) or bf16 rows
+  const void* V;
+  const void* Kp;  // row words of a 4-bit cache, else null
+  const void* Vp;
+  const int32_t* seqlens;
+  void* out;
+  const float* w_in;  // [B, Hkv, L]; w_out null: no weights
+  float* w_out;
+  int B, H, Hkv, L, d;
+  int splits;       // CTAs a (b, KV head)
+  float* partials;  // records [B*Hkv, splits, G, 2d + 4]; null: the splits are a cluster
+  float* scores;    // log2-domain scores [B*Hkv, L, G] (weights only)
+  int* status;
+};
+struct CacheDecodeSpace {
+  int splits = 1;
+  size_t partials = 0, scores = 0;  // bytes, the scores behind the partials
+};
+CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool weights);
+cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t st);
+
+// Eviction (cache_evict.cu).
+constexpr int kEvictMaxCaches = 8;
+struct EvictArgs {
+  int count;                          // caches
+  const void* src[kEvictMaxCaches];   // [B, Hkv, L] rows
+  void* dst[kEvictMaxCaches];         // [B, Hkv, Lout] rows, or src itself (then Lout == L)
+  int row_bytes[kEvictMaxCaches];
+  const float* w;        // [B, Hkv, L]
+  float* w_out;          // [B, Hkv, Lout]
+  const int32_t* seqlens;
+  int32_t* seqlens_out;
+  int32_t* kept;         // [B, Hkv, min(budget, L)]
+  int B, Hkv, L, Lout, budget, sinks, recent;
+  int* status;
+};
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st, int num_sms);
+
 }  // namespace plx
 
 namespace plx {

@@ -8,6 +8,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -56,6 +57,15 @@ SIGNATURES = {
     "plx_kv_quantize_fp8": (_i, [_vp, _vp, _vp, ctypes.c_longlong, _i, _vp]),
     "plx_decode_fp8kv_workspace_bytes": (_sz, [_i] * 5),
     "plx_decode_fp8kv": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _sz, _vp]),
+    "plx_kv_quantize_int4": (_i, [_vp] * 3 + [ctypes.c_longlong, _i, _vp]),
+    "plx_kv_dequantize_int4": (_i, [_vp] * 3 + [ctypes.c_longlong, _i, _vp]),
+    "plx_kv_append_int4": (_i, [_vp] * 9 + [_i] * 4 + [_vp]),
+    "plx_decode_int4kv_workspace_bytes": (_sz, [_i] * 5),
+    "plx_decode_int4kv": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _sz, _vp]),
+    "plx_decode_weights_workspace_bytes": (_sz, [_i] * 5),
+    "plx_decode_weights": (_i, [_vp] * 8 + [_i] * 5 + [_vp, _sz, _vp]),
+    "plx_decode_int4kv_weights": (_i, [_vp] * 10 + [_i] * 5 + [_vp, _sz, _vp]),
+    "plx_cache_evict": (_i, [_i] + [_vp] * 8 + [_i] * 7 + [_vp]),
     "plx_get_device_status": (_i, [_vp]),
     "plx_status_string": (ctypes.c_char_p, [_i]),
     "plx_last_cuda_error": (ctypes.c_char_p, []),
@@ -434,6 +444,225 @@ def decode_fp8kv(q, r, Kcodes, Kscales, Vcodes, Vscales, seqlens, out=None, work
                               _dev(out, "out"), B, H, Hkv, L, d, ws_ptr, ws_bytes, _stream_ptr(stream))
     _check(rc, "plx_decode_fp8kv")
     return out
+
+
+class _Launch:
+    """Where a call runs: the device all its tensors are on, and the given or that device's current stream.
+
+    A context manager: inside it that device and stream are torch's current ones, so that what is
+    allocated there may be used on the stream at once.  ptr() checks a tensor and returns its address."""
+
+    __slots__ = ("device", "stream", "_guards")
+
+    def __init__(self, first, stream):
+        if not first.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        self.device = first.device
+        self.stream = stream
+        if stream is not None and stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+
+    def __enter__(self):
+        self._guards = []
+        if self.stream is not None:
+            self._guards.append(torch.cuda.stream(self.stream))
+        elif self.device.index != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(self.device))
+        for guard in self._guards:
+            guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for guard in reversed(self._guards):
+            guard.__exit__(*exc)
+
+    def ptr(self, t, name: str, shape, dtype) -> int:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {self.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def workspace(self, given, need: int):
+        """(tensor that keeps it alive, address, bytes) of the caller's workspace or a new one."""
+        if given is None:
+            if need == 0:
+                return None, None, 0
+            given = torch.empty(need, dtype=torch.uint8, device=self.device)
+        elif given.device != self.device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {self.device}")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+
+    def raw_stream(self) -> int:
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+
+def kv_quantize_int4(X, codes=None, params=None, stream=None):
+    """4-bit rows of bf16 cache rows X [..., d]: returns (codes uint8 [..., d/2], params bf16 [..., 2]),
+    each row standing for scale * (code - zero point) with (scale, zero point) its params."""
+    d = X.shape[-1]
+    lead = X.shape[:-1]
+    with _Launch(X, stream) as on:
+        if codes is None:
+            codes = torch.empty((*lead, d // 2), dtype=torch.uint8, device=X.device)
+        if params is None:
+            params = torch.empty((*lead, 2), dtype=torch.bfloat16, device=X.device)
+        rc = lib.plx_kv_quantize_int4(on.ptr(X, "X", X.shape, torch.bfloat16),
+                                      on.ptr(codes, "codes", (*lead, d // 2), torch.uint8),
+                                      on.ptr(params, "params", (*lead, 2), torch.bfloat16),
+                                      X.numel() // d, d, on.raw_stream())
+    _check(rc, "plx_kv_quantize_int4")
+    return codes, params
+
+
+def kv_dequantize_int4(codes, params, out=None, stream=None):
+    """The bf16 values [..., d] that 4-bit rows stand for: codes uint8 [..., d/2], params bf16 [..., 2]."""
+    lead, d = codes.shape[:-1], 2 * codes.shape[-1]
+    with _Launch(codes, stream) as on:
+        if out is None:
+            out = torch.empty((*lead, d), dtype=torch.bfloat16, device=codes.device)
+        rc = lib.plx_kv_dequantize_int4(on.ptr(codes, "codes", codes.shape, torch.uint8),
+                                        on.ptr(params, "params", (*lead, 2), torch.bfloat16),
+                                        on.ptr(out, "out", (*lead, d), torch.bfloat16),
+                                        codes.numel() // (d // 2), d, on.raw_stream())
+    _check(rc, "plx_kv_dequantize_int4")
+    return out
+
+
+def _int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d):
+    rows, words = (B, Hkv, L, d // 2), (B, Hkv, L, 2)
+    return (on.ptr(Kcodes, "Kcodes", rows, torch.uint8), on.ptr(Kparams, "Kparams", words, torch.bfloat16),
+            on.ptr(Vcodes, "Vcodes", rows, torch.uint8), on.ptr(Vparams, "Vparams", words, torch.bfloat16))
+
+
+def kv_append_int4(k, v, Kcodes, Kparams, Vcodes, Vparams, seqlens, k_out=None, v_out=None, stream=None):
+    """Writes the new rows k, v bf16 [B, Hkv, d] to row seqlens - 1 of a 4-bit cache (codes uint8
+    [B, Hkv, L, d/2], params bf16 [B, Hkv, L, 2]); k_out, v_out, if given, get the values they stand for."""
+    B, Hkv, d = k.shape
+    L = Kcodes.shape[2]
+    new = (B, Hkv, d)
+    with _Launch(k, stream) as on:
+        rc = lib.plx_kv_append_int4(on.ptr(k, "k", new, torch.bfloat16), on.ptr(v, "v", new, torch.bfloat16),
+                                    *_int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d),
+                                    on.ptr(seqlens, "seqlens", (B,), torch.int32),
+                                    None if k_out is None else on.ptr(k_out, "k_out", new, torch.bfloat16),
+                                    None if v_out is None else on.ptr(v_out, "v_out", new, torch.bfloat16),
+                                    B, Hkv, L, d, on.raw_stream())
+    _check(rc, "plx_kv_append_int4")
+
+
+def decode_int4kv_workspace_bytes(B: int, H: int, Hkv: int, L: int, d: int) -> int:
+    return int(lib.plx_decode_int4kv_workspace_bytes(B, H, Hkv, L, d))
+
+
+def decode_int4kv(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, out=None, workspace=None, stream=None):
+    """Decode over a 4-bit cache: q, r bf16 [B, H, d]; codes uint8 [B, Hkv, L, d/2]; params bf16
+    [B, Hkv, L, 2]; seqlens int32 [B]."""
+    B, H, d = q.shape
+    Hkv, L = Kcodes.shape[1], Kcodes.shape[2]
+    with _Launch(q, stream) as on:
+        if out is None:
+            out = torch.empty_like(q)
+        ws, ws_ptr, ws_bytes = on.workspace(workspace, lib.plx_decode_int4kv_workspace_bytes(B, H, Hkv, L, d))
+        rc = lib.plx_decode_int4kv(on.ptr(q, "q", q.shape, torch.bfloat16), on.ptr(r, "r", q.shape, torch.bfloat16),
+                                   *_int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d),
+                                   on.ptr(seqlens, "seqlens", (B,), torch.int32),
+                                   on.ptr(out, "out", q.shape, torch.bfloat16),
+                                   B, H, Hkv, L, d, ws_ptr, ws_bytes, on.raw_stream())
+    _check(rc, "plx_decode_int4kv")
+    return out
+
+
+def decode_weights_workspace_bytes(B: int, H: int, Hkv: int, L: int, d: int) -> int:
+    return int(lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d))
+
+
+def decode_weights(q, r, Kcache, Vcache, seqlens, weights, weights_out=None, out=None, workspace=None, stream=None):
+    """decode_gqa that also writes weights_out = weights + every visible key's softmax weight, summed over
+    the query heads of its KV head (fp32 [B, Hkv, L]; weights itself when None); returns out."""
+    B, Hkv, L, d = Kcache.shape
+    H = q.shape[1]
+    cache, totals = (B, Hkv, L, d), (B, Hkv, L)
+    with _Launch(q, stream) as on:
+        if out is None:
+            out = torch.empty_like(q)
+        if weights_out is None:
+            weights_out = weights
+        ws, ws_ptr, ws_bytes = on.workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d))
+        rc = lib.plx_decode_weights(on.ptr(q, "q", (B, H, d), torch.bfloat16),
+                                    on.ptr(r, "r", (B, H, d), torch.bfloat16),
+                                    on.ptr(Kcache, "Kcache", cache, torch.bfloat16),
+                                    on.ptr(Vcache, "Vcache", cache, torch.bfloat16),
+                                    on.ptr(seqlens, "seqlens", (B,), torch.int32),
+                                    on.ptr(weights, "weights", totals, torch.float32),
+                                    on.ptr(weights_out, "weights_out", totals, torch.float32),
+                                    on.ptr(out, "out", (B, H, d), torch.bfloat16),
+                                    B, H, Hkv, L, d, ws_ptr, ws_bytes, on.raw_stream())
+    _check(rc, "plx_decode_weights")
+    return out
+
+
+def decode_int4kv_weights(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, weights, weights_out=None, out=None,
+                          workspace=None, stream=None):
+    """decode_weights over a 4-bit cache (decode_int4kv)."""
+    B, H, d = q.shape
+    Hkv, L = Kcodes.shape[1], Kcodes.shape[2]
+    totals = (B, Hkv, L)
+    with _Launch(q, stream) as on:
+        if out is None:
+            out = torch.empty_like(q)
+        if weights_out is None:
+            weights_out = weights
+        ws, ws_ptr, ws_bytes = on.workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d))
+        rc = lib.plx_decode_int4kv_weights(on.ptr(q, "q", q.shape, torch.bfloat16),
+                                           on.ptr(r, "r", q.shape, torch.bfloat16),
+                                           *_int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d),
+                                           on.ptr(seqlens, "seqlens", (B,), torch.int32),
+                                           on.ptr(weights, "weights", totals, torch.float32),
+                                           on.ptr(weights_out, "weights_out", totals, torch.float32),
+                                           on.ptr(out, "out", q.shape, torch.bfloat16),
+                                           B, H, Hkv, L, d, ws_ptr, ws_bytes, on.raw_stream())
+    _check(rc, "plx_decode_int4kv_weights")
+    return out
+
+
+def cache_evict(caches, weights, seqlens, budget: int, sinks: int = 0, recent: int = 0, caches_out=None,
+                weights_out=None, seqlens_out=None, stream=None):
+    """Cuts every sequence longer than ``budget`` to its first ``sinks`` rows, its last ``recent`` rows and the
+    rows of largest weight between them, for each KV head on its own.
+
+    caches: tensors [B, Hkv, L, ...] of any type (keys, values, codes, params, scales); weights fp32
+    [B, Hkv, L]; seqlens int32 [B].  Rows move, in the order of their positions, to caches_out
+    [B, Hkv, L_out, ...] and weights_out [B, Hkv, L_out] (0 behind the last), L_out >= min(budget, L); both in
+    place when None.  Returns (kept int32 [B, Hkv, min(budget, L)], the rows' old positions, -1 behind the
+    last; new seqlens int32 [B])."""
+    B, Hkv, L = weights.shape
+    caches = tuple(caches)
+    in_place = caches_out is None
+    if in_place != (weights_out is None):
+        raise ValueError("caches_out and weights_out go together: both given, or both None (in place)")
+    caches_out, weights_out = (caches, weights) if in_place else (tuple(caches_out), weights_out)
+    if len(caches_out) != len(caches):
+        raise ValueError("caches_out must hold one tensor for each of caches")
+    L_out = weights_out.shape[-1]
+    n = len(caches)
+    with _Launch(weights, stream) as on:
+        kept = torch.empty((B, Hkv, min(max(budget, 0), L)), dtype=torch.int32, device=weights.device)
+        if seqlens_out is None:
+            seqlens_out = torch.empty((B,), dtype=torch.int32, device=weights.device)
+        src = [on.ptr(t, "caches", (B, Hkv, L, *t.shape[3:]), t.dtype) for t in caches]
+        dst = [on.ptr(o, "caches_out", (B, Hkv, L_out, *t.shape[3:]), t.dtype) for t, o in zip(caches, caches_out)]
+        row = [t.element_size() * math.prod(t.shape[3:]) for t in caches]
+        rc = lib.plx_cache_evict(n, (_vp * n)(*src), (_vp * n)(*dst), (_i * n)(*row),
+                                 on.ptr(weights, "weights", (B, Hkv, L), torch.float32),
+                                 on.ptr(weights_out, "weights_out", (B, Hkv, L_out), torch.float32),
+                                 on.ptr(seqlens, "seqlens", (B,), torch.int32),
+                                 on.ptr(seqlens_out, "seqlens_out", (B,), torch.int32),
+                                 kept.data_ptr(), B, Hkv, L, L_out, budget, sinks, recent, on.raw_stream())
+    _check(rc, "plx_cache_evict")
+    return kept, seqlens_out
 
 
 def qkr_norm_rope(x, H: int, eps: float = 1e-6, base: float = 10000.0, out=None, stream=None):

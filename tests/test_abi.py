@@ -196,3 +196,75 @@ def test_layer_workspace_slots_match_the_binding():
             t = views[name]
             assert t.dtype == torch.bfloat16 and tuple(t.shape) == (B, H, N, d)
             assert t.data_ptr() - base == (4 + i) * slot
+
+
+def test_int4_cache_calls_reject_bad_arguments(lib):
+    # plx_kv_quantize_int4(X, codes, params, rows, d, stream)
+    for call in (lib.plx_kv_quantize_int4, lib.plx_kv_dequantize_int4):
+        assert call(None, A, A, 4, 128, None) == -1
+        assert call(A, A, A, 0, 128, None) == -1
+        assert call(A, A, A, 4, 96, None) == -2
+        assert call(A + 8, A, A, 4, 128, None) == -3
+    assert lib.plx_kv_quantize_int4(A, A, A + 2, 4, 128, None) == -3
+    # plx_kv_append_int4(k, v, Kc, Kp, Vc, Vp, seqlens, k_out, v_out, B, Hkv, L, d, stream)
+    ok = [A] * 9
+    assert lib.plx_kv_append_int4(A, A, A, A, A, None, A, None, None, 1, 2, 8, 128, None) == -1
+    assert lib.plx_kv_append_int4(*ok, 1, 0, 8, 128, None) == -1
+    assert lib.plx_kv_append_int4(*ok, 1, 2, 8, 32, None) == -2
+    assert lib.plx_kv_append_int4(A, A, A, A, A, A, A, A + 8, None, 1, 2, 8, 128, None) == -3
+    assert lib.plx_kv_append_int4(*ok, 1 << 20, 16, 200, 128, None) == -2
+
+
+def test_cache_decodes_reject_bad_arguments(lib):
+    # plx_decode_int4kv(q, r, Kc, Kp, Vc, Vp, seqlens, out, B, H, Hkv, L, d, ws, ws_bytes, stream)
+    tail = (None, 0, None)
+    ok8, ok10 = [A] * 8, [A] * 9 + [A]
+    B5 = 0x500000  # a second array apart from the first
+    w10 = [A] * 7 + [A, B5, A]    # ... seqlens, weights, weights_out, out
+    w8 = [A] * 5 + [A, B5, A]
+    for call, ok in ((lib.plx_decode_int4kv, ok8), (lib.plx_decode_int4kv_weights, w10), (lib.plx_decode_weights, w8)):
+        for i in range(len(ok)):
+            assert call(*ok[:i], None, *ok[i + 1:], 1, 8, 2, 64, 128, *tail) == -1
+        assert call(*ok, 1, 8, 3, 64, 128, *tail) == -1    # H not a multiple of Hkv
+        assert call(*ok, 0, 8, 2, 64, 128, *tail) == -1
+        assert call(*ok, 1, 6, 2, 64, 128, *tail) == -2    # group of 3
+        assert call(*ok, 1, 32, 2, 64, 128, *tail) == -2   # group of 16
+        assert call(*ok, 1, 8, 2, 64, 96, *tail) == -2
+        assert call(*ok, 1 << 22, 8, 8, 64, 128, *tail) == -2
+        assert call(*ok, 4, 64, 16, ((1 << 31) - 128) // 64, 128, *tail) == -2
+        assert call(A + 8, *ok[1:], 1, 8, 2, 64, 128, *tail) == -3
+    assert lib.plx_decode_int4kv(A, A, A, A + 2, A, A, A, A, 1, 8, 2, 64, 128, *tail) == -3   # params 4 B
+    # weights and weights_out overlap without being the same
+    assert lib.plx_decode_weights(*[A] * 6, A + 64, A, 1, 8, 2, 64, 128, *tail) == -1
+    assert lib.plx_decode_int4kv_workspace_bytes(1, 8, 3, 64, 128) == 0
+    assert lib.plx_decode_weights_workspace_bytes(1, 8, 2, 64, 128) >= 8 * 64 * 4
+    assert lib.plx_decode_int4kv_workspace_bytes(64, 16, 16, 4096, 128) == 0
+    assert lib.plx_decode_int4kv_workspace_bytes(1, 1, 1, 1 << 20, 128) > 0
+
+
+def test_cache_evict_rejects_bad_arguments(lib):
+    """Checked on the host: sizes, the rule's numbers, overlaps of caches, totals and outputs."""
+    vp, it = ctypes.c_void_p, ctypes.c_int
+
+    def call(src=(A,), dst=(0x900000,), row=(256,), w=0x2000000, wo=0x3000000, B=1, Hkv=2, L=64, Lout=16, budget=16,
+             sinks=1, recent=2, count=None, sl=A, kept=A):
+        n = len(src)
+        return lib.plx_cache_evict(n if count is None else count, (vp * max(n, 1))(*src), (vp * max(n, 1))(*dst),
+                                   (it * max(n, 1))(*row), w, wo, sl, sl, kept, B, Hkv, L, Lout, budget, sinks,
+                                   recent, None)
+
+    for kw in (dict(w=None), dict(wo=None), dict(sl=None), dict(kept=None), dict(count=-1), dict(B=0), dict(L=0),
+               dict(budget=0), dict(sinks=-1), dict(recent=-1), dict(sinks=10, recent=7), dict(Lout=15),
+               dict(row=(0,)), dict(src=(None,)), dict(dst=(None,)),
+               dict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1),
+               dict(dst=(A,)),                                   # in place needs L_out = L
+               dict(dst=(A + 256,)), dict(wo=0x2000000 + 4),     # partly over itself
+               dict(src=(A, A), dst=(A, A), row=(4, 4), Lout=64),  # one buffer twice
+               dict(src=(A, 0x700000), dst=(0x900000, 0x900010), row=(256, 256)),
+               dict(dst=(0x2000000,))):                          # over the totals
+        assert call(**kw) == -1, kw
+    assert call(row=(65537,), dst=(0x90000000,)) == -2
+    assert call(src=[A * 16 * i for i in range(1, 10)], dst=[A * 4096 * i for i in range(1, 10)], row=[4] * 9,
+                w=0x200000000, wo=0x300000000) == -2
+    assert call(B=1 << 20, Hkv=32, w=0x20000000000, wo=0x30000000000) == -2
+    assert call(w=0x2000002) == -3
