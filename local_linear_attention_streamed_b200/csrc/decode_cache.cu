@@ -23,12 +23,12 @@
 //   [w s_v, w t s_v] packs into one register, and movmatrix turns the score
 //   layout into the value MMA's operand.  Measured rate: one MMA in 2.0 clocks
 //   an SM.
-// * Codes become bf16 in two instructions a pair: AND picks two nibbles, which
-//   as bf16 bits are c 2^-133 (or c 2^-129: bits 4..7 still lie in the linear
-//   range of bf16), and one FMA turns them into (c - z) 2^-6, exactly.  The
-//   zero point is thus gone before the sums: summing raw codes and subtracting
-//   z omega afterwards would lose the small differences of large sums.  The
-//   dims are paired as the nibbles fall; the other operand is permuted to match.
+// * AND picks two nibbles of a code word, and these bits are bf16 numbers:
+//   c 2^-133 (or c 2^-129: bits 4..7 still lie in the linear range of bf16).
+//   Key codes go into the MMA as such, against queries scaled by a power of two;
+//   z (sum of q) goes off each score.  Value codes become (c - z) 2^-6 in one FMA
+//   first, exactly: sums over raw codes would be large, with small differences.
+//   The dims are paired as the nibbles fall; the other operand is permuted to match.
 // * Groups of 1 and 2 leave columns free: the weights go in as bf16 hi + lo
 //   pairs there; larger groups issue a second MMA for the lo part.  So the
 //   weights keep 16 bits.
@@ -37,11 +37,15 @@
 // * Each warp runs its own ring of key tiles with cp.async (no block barrier in
 //   the loop, no wait that could not end) and its own partial state.
 //
-// The keys of a sequence are cut evenly (by its own length) over `splits` CTAs.
-// Up to 8 splits are a cluster and merge through distributed shared memory; a
-// larger number, and every decode with weights, writes partial records to the
-// caller's workspace, and a second kernel merges them.  There are no counters
-// and no library-owned memory: calls on several streams are independent.
+// Three ways to cut the keys (cache_decode_space chooses): one CTA a (b, KV head);
+// a cluster of CTAs, merged through distributed shared memory; or all tiles of the
+// batch in equal shares, one a warp, with partial records in the caller's
+// workspace that a second kernel merges.  There are no counters and no
+// library-owned memory: calls on several streams are independent.
+//
+// What bounds it now: instructions.  15.5 a key and warp at G = 1, d = 128 (ALU
+// pipe 55 %, MMA pipe 31 %, issue slots 59 % busy with the 16 warps that registers
+// allow): 64 x 16 sequences of 4096 keys take 103 us, 5.5 TB/s, 0.85 of a copy's rate.
 #include "plx_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -60,11 +64,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same onto zeros.
+__device__ __forceinline__ void mma_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
@@ -79,11 +92,17 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "r"(addr));
 }
 
-// 16- or 4-byte asynchronous copy; ok == false fills zeros and reads nothing.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+// 16- and 4-byte asynchronous copies; in the z forms ok == false fills zeros and reads nothing.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16z(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool ok) {
+__device__ __forceinline__ void cp4z(uint32_t dst, const void* src, bool ok) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -115,18 +134,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Two nibbles to (c - z) 2^-6: kEven picks bits 0..3 and 16..19 of x, kOdd bits
-// 4..7 and 20..23.  mz = (-z 2^-6) in both halves (or one for each half's key).
+// Two nibbles of x as bf16: kEven picks bits 0..3 and 16..19, kOdd bits 4..7
+// and 20..23; they read as c 2^-133 and c 2^-129.  nib_*: (c - z) 2^-6, with
+// mz = (-z 2^-6) of each half's key.
+constexpr uint32_t kEven = 0x000f000fu, kOdd = 0x00f000f0u;
 constexpr uint32_t kScaleEven = 0x7f007f00u;  // 2^127: c 2^-133 -> c 2^-6
 constexpr uint32_t kScaleOdd = 0x7d007d00u;   // 2^123: c 2^-129 -> c 2^-6
 __device__ __forceinline__ uint32_t nib_even(uint32_t x, uint32_t mz) {
-  return fma_bf16x2(x & 0x000f000fu, kScaleEven, mz);
+  return fma_bf16x2(x & kEven, kScaleEven, mz);
 }
 __device__ __forceinline__ uint32_t nib_odd(uint32_t x, uint32_t mz) {
-  return fma_bf16x2(x & 0x00f000f0u, kScaleOdd, mz);
+  return fma_bf16x2(x & kOdd, kScaleOdd, mz);
 }
 __device__ __forceinline__ uint32_t neg_zero_points(uint32_t z2) {  // (z, z') -> (-z 2^-6, -z' 2^-6)
   return fma_bf16x2(z2, 0xbc80bc80u, 0u);
@@ -139,11 +165,11 @@ struct Tile {
   static constexpr int kKeys = I4 ? 32 : 2048 / D;        // keys of a stage
   static constexpr int kStages = 3;
   static constexpr int kChunks = kRow / 16;               // 16-byte pieces of a row
-  static constexpr int kVOff = kKeys * kRow;              // a stage: K rows, V rows, K words, V words
+  static constexpr int kVOff = kKeys * kRow;              // a stage: K rows, V rows, (K word, V word) of every key
   static constexpr int kPOff = 2 * kKeys * kRow;
   static constexpr int kBytes = kPOff + (I4 ? 8 * kKeys : 0);
   static constexpr int kWarpBytes = kStages * kBytes;
-  static constexpr int kSmem = kWarps * kWarpBytes;
+  static constexpr int kRing = kWarps * kWarpBytes;
 };
 
 // Where a V row and its 16-byte pieces sit in a stage.  4-bit: lane t reads
@@ -170,27 +196,61 @@ __device__ __forceinline__ int k_place(int key, int chunk) {
   }
 }
 
+// A lane's part of its warp's tile copies: 32 pieces of 16 bytes a step, so every
+// step is 512 bytes further on both sides (4-bit rows; bf16 V pieces move within
+// their row with the key).
 template <bool I4, int D>
-__device__ __forceinline__ void load_tile(uint32_t stage, const CacheDecodeArgs& a, size_t row0, int j0, int n,
-                                          int lane) {
+struct Loader {
   using T = Tile<I4, D>;
-  const char* K = static_cast<const char*>(a.K) + (row0 + j0) * T::kRow;
-  const char* V = static_cast<const char*>(a.V) + (row0 + j0) * T::kRow;
+  static constexpr int kSteps = T::kKeys * T::kChunks / 32;
+  int key0, c;
+  uint32_t kdst, vdst;
+
+  __device__ __forceinline__ explicit Loader(int lane) {
+    key0 = lane / T::kChunks;
+    c = lane % T::kChunks;
+    kdst = k_place<I4, D>(key0, c);
+    vdst = T::kVOff + v_place<I4, D>(key0, c);
+  }
+  // The tile whose first row is `row` of all cache rows, `left` rows before the sequence's end.
+  __device__ __forceinline__ void copy(const CacheDecodeArgs& a, uint32_t stage, int row, int left, int lane) const {
+    constexpr int kStep = 32 / T::kChunks;  // keys a step
+    const char* K = static_cast<const char*>(a.K) + (size_t)row * T::kRow;
+    const char* V = static_cast<const char*>(a.V) + (size_t)row * T::kRow;
+    const char* Kp = static_cast<const char*>(a.Kp) + (size_t)row * 4;
+    const char* Vp = static_cast<const char*>(a.Vp) + (size_t)row * 4;
+    if (left >= T::kKeys) {
+      K += lane * 16;
+      V += lane * 16;
 #pragma unroll
-  for (int i = lane; i < T::kKeys * T::kChunks; i += 32) {
-    const int key = i / T::kChunks, c = i % T::kChunks;
-    const bool ok = j0 + key < n;
-    const size_t off = ok ? (size_t)i * 16 : 0;
-    cp16(stage + k_place<I4, D>(key, c), K + off, ok);
-    cp16(stage + T::kVOff + v_place<I4, D>(key, c), V + off, ok);
+      for (int i = 0; i < kSteps; ++i) {
+        cp16(stage + kdst + 512 * i, K + 512 * i);
+        if constexpr (I4) {
+          cp16(stage + vdst + 512 * i, V + 512 * i);
+        } else {
+          cp16(stage + T::kVOff + v_place<I4, D>(key0 + kStep * i, c), V + 512 * i);
+        }
+      }
+      if constexpr (I4) {
+        cp4(stage + T::kPOff + 8 * lane, Kp + 4 * lane);
+        cp4(stage + T::kPOff + 8 * lane + 4, Vp + 4 * lane);
+      }
+    } else {  // the sequence's last tile: rows behind the end are zeros, and are not read
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const bool ok = key0 + kStep * i < left;
+        const int off = ok ? 512 * i + 16 * lane : 0;
+        cp16z(stage + k_place<I4, D>(key0 + kStep * i, c), K + off, ok);
+        cp16z(stage + T::kVOff + v_place<I4, D>(key0 + kStep * i, c), V + off, ok);
+      }
+      if constexpr (I4) {
+        const bool ok = lane < left;
+        cp4z(stage + T::kPOff + 8 * lane, Kp + (ok ? 4 * lane : 0), ok);
+        cp4z(stage + T::kPOff + 8 * lane + 4, Vp + (ok ? 4 * lane : 0), ok);
+      }
+    }
   }
-  if constexpr (I4) {
-    const bool ok = j0 + lane < n;
-    const size_t off = (row0 + j0 + (ok ? lane : 0)) * 4;
-    cp4(stage + T::kPOff + 4 * lane, static_cast<const char*>(a.Kp) + off, ok);
-    cp4(stage + T::kPOff + 4 * T::kKeys + 4 * lane, static_cast<const char*>(a.Vp) + off, ok);
-  }
-}
+};
 
 // Partial state of one warp for NT column tiles (four heads each).
 template <int D, int NT>
@@ -199,95 +259,241 @@ struct State {
   float m[NT], omega[NT], T[NT];
 };
 
-template <bool I4, int D, int G, bool W>
-__device__ __forceinline__ void compute_block(State<D, (G + 3) / 4>& s, uint32_t stage, int blk,
-                                              const uint32_t (&qf)[(G + 3) / 4][D / 16][2], float cs,
-                                              float* __restrict__ scores, int j0, int n, int lane) {
-  using T = Tile<I4, D>;
-  constexpr int NT = (G + 3) / 4, KS = D / 16;
+// The query rows as MMA columns: column g is q (even) or rho (odd) of head g/2 of
+// the column tile (modulo G).  4-bit: a row x goes in as x 2^(126 - E), E the
+// exponent of its largest element, and over 16 for the odd nibbles, so that sums
+// over raw codes are (sum of x c) 2^(-7 - E); all of it exact.  sum and scale
+// belong to the lane's own columns 2t and 2t + 1.
+template <int D, int NT>
+struct Query {
+  uint32_t b[NT][D / 16][2];
+  float sum[NT][2];    // (sum of x) 2^(-7 - E)
+  float scale[NT][2];  // 2^(7 + E), with log2(e) / sqrt(d) for q
+  float cs;
+};
+
+template <int D, int G>
+__device__ __forceinline__ void load_query_int4(Query<D, (G + 3) / 4>& q, const __nv_bfloat16* qrow,
+                                                const __nv_bfloat16* rrow, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  const int kb = 16 * blk;
-  // ---- scores: rows = keys g, g + 8; columns = q, rho of the heads.
-  float S[NT][2][4];
 #pragma unroll
-  for (int u = 0; u < NT; ++u)
+  for (int u = 0; u < (G + 3) / 4; ++u) {
+    const int h = (G >= 4) ? 4 * u + (g >> 1) : (g >> 1) % G;
+    const uint4* row = reinterpret_cast<const uint4*>(((g & 1) ? rrow : qrow) + h * D) + (D / 32) * t;
+    uint4 v[D / 32];  // the eight dims of each code word
+    uint32_t top = 0;  // largest magnitude, as bits
 #pragma unroll
-    for (int e = 0; e < 4; ++e) S[u][0][e] = S[u][1][e] = 0.f;
-  uint32_t pk[2] = {0u, 0u};
+    for (int i = 0; i < D / 32; ++i) {
+      v[i] = row[i];
+      const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // Subnormal rows take the exponent of the smallest normal number.
+    const int E = top >= 0x00800000u ? (int)(top >> 23) - 127 : -126;
+    // 2^-E in two factors, each a normal number (E in [-126, 128]).
+    const float f0 = __uint_as_float((uint32_t)(127 - (E >> 1)) << 23);
+    const float f1 = __uint_as_float((uint32_t)(127 - (E - (E >> 1))) << 23);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[2 * e] = bf_lo(x[e]) * f0 * f1;
+        y[2 * e + 1] = bf_hi(x[e]) * f0 * f1;
+        sum += y[2 * e] + y[2 * e + 1];
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        q.b[u][2 * i + p][0] = pack_bf16(y[2 * p] * 0x1p126f, y[2 * p + 4] * 0x1p126f);
+        q.b[u][2 * i + p][1] = pack_bf16(y[2 * p + 1] * 0x1p122f, y[2 * p + 5] * 0x1p122f);
+      }
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    sum *= 0x1p-7f;
+    // 2^(7 + E), as 2^7 2^E: E = 121 and above (rows beyond 2^121) overflow to infinity.
+    const float up = __uint_as_float((uint32_t)(min(E, 127) + 127) << 23) * 128.f * ((g & 1) ? 1.f : q.cs);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      q.sum[u][e] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+      q.scale[u][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t + e));
+    }
+  }
+}
+
+template <int D, int G>
+__device__ __forceinline__ void load_query_bf16(Query<D, (G + 3) / 4>& q, const __nv_bfloat16* qrow,
+                                                const __nv_bfloat16* rrow, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int u = 0; u < (G + 3) / 4; ++u) {
+    const int h = (G >= 4) ? 4 * u + (g >> 1) : (g >> 1) % G;
+    const uint4* row = reinterpret_cast<const uint4*>(((g & 1) ? rrow : qrow) + h * D);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = row[4 * i + t];
+      q.b[u][2 * i][0] = v.x;
+      q.b[u][2 * i][1] = v.y;
+      q.b[u][2 * i + 1][0] = v.z;
+      q.b[u][2 * i + 1][1] = v.w;
+    }
+  }
+}
+
+// Rows of (b, KV head) `unit` as q, and an empty state.
+template <bool I4, int D, int G>
+__device__ __forceinline__ void begin_unit(const CacheDecodeArgs& a, Query<D, (G + 3) / 4>& q,
+                                           State<D, (G + 3) / 4>& s, int unit, int lane) {
+  const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + (size_t)unit * G * D;
+  const __nv_bfloat16* rrow = static_cast<const __nv_bfloat16*>(a.r) + (size_t)unit * G * D;
+  if constexpr (I4) {
+    load_query_int4<D, G>(q, qrow, rrow, lane);
+  } else {
+    load_query_bf16<D, G>(q, qrow, rrow, lane);
+  }
+#pragma unroll
+  for (int u = 0; u < (G + 3) / 4; ++u) {
+    s.m[u] = kNoRef;
+    s.omega[u] = s.T[u] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s.O[u][i][e] = 0.f;
+  }
+}
+
+// Score accumulators of a tile: rows = keys g, g + 8 of a block, columns = q, rho
+// of the heads.  Two short MMA chains a block where there are registers for them.
+template <bool I4, int D, int G>
+struct Scores {
+  static constexpr int NT = (G + 3) / 4, NB = Tile<I4, D>::kKeys / 16, NC = NT * NB <= 2 ? 2 : 1;
+  float S[NB][NT][NC][4];
+};
+
+// Scores of block b of the tile in `stage`.
+template <bool I4, int D, int G>
+__device__ __forceinline__ void score_block(Scores<I4, D, G>& sc, uint32_t stage, const Query<D, (G + 3) / 4>& q,
+                                            int b, int lane) {
+  using T = Tile<I4, D>;
+  using Sc = Scores<I4, D, G>;
+  constexpr int NT = Sc::NT, NC = Sc::NC;
+  const int g = lane >> 2, t = lane & 3;
+  auto mma = [&](int u, int step, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+    if (step < NC) {
+      mma_bf16_first(sc.S[b][u][step], a0, a1, a2, a3, q.b[u][step][0], q.b[u][step][1]);
+    } else {
+      mma_bf16(sc.S[b][u][step % NC], a0, a1, a2, a3, q.b[u][step][0], q.b[u][step][1]);
+    }
+  };
   if constexpr (I4) {
     constexpr int WPL = D / 32;  // code words a lane has of a key
-    uint32_t w[2][4], mz[2];
+    uint32_t w[2][WPL];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint32_t at = stage + (kb + g + 8 * r) * T::kRow + 4 * WPL * t;
+      const uint32_t at = stage + (16 * b + g + 8 * r) * T::kRow + 4 * WPL * t;
       if constexpr (WPL == 4) {
         lds128(w[r], at);
       } else {
         lds64(w[r][0], w[r][1], at);
       }
-      pk[r] = lds32(stage + T::kPOff + 4 * (kb + g + 8 * r));
-      mz[r] = neg_zero_points(__byte_perm(pk[r], 0, 0x3232));
     }
 #pragma unroll
-    for (int i = 0; i < WPL; ++i) {
+    for (int i = 0; i < WPL; ++i)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const uint32_t x0 = p ? w[0][i] >> 8 : w[0][i], x1 = p ? w[1][i] >> 8 : w[1][i];
-        const uint32_t a0 = nib_even(x0, mz[0]), a1 = nib_even(x1, mz[1]);
-        const uint32_t a2 = nib_odd(x0, mz[0]), a3 = nib_odd(x1, mz[1]);
 #pragma unroll
-        for (int u = 0; u < NT; ++u) mma_bf16(S[u][p], a0, a1, a2, a3, qf[u][2 * i + p][0], qf[u][2 * i + p][1]);
+        for (int u = 0; u < NT; ++u)
+          mma(u, 2 * i + p, x0 & kEven, x1 & kEven, x0 & kOdd, x1 & kOdd);
       }
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t x[4], y[4];
-      lds128(x, stage + k_place<I4, D>(kb + g, 4 * i + t));
-      lds128(y, stage + k_place<I4, D>(kb + g + 8, 4 * i + t));
+      lds128(x, stage + k_place<I4, D>(16 * b + g, 4 * i + t));
+      lds128(y, stage + k_place<I4, D>(16 * b + g + 8, 4 * i + t));
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int u = 0; u < NT; ++u)
-          mma_bf16(S[u][p], x[2 * p], y[2 * p], x[2 * p + 1], y[2 * p + 1], qf[u][2 * i + p][0],
-                   qf[u][2 * i + p][1]);
+          mma(u, 2 * i + p, x[2 * p], y[2 * p], x[2 * p + 1], y[2 * p + 1]);
     }
   }
-  // ---- weights.
-  uint32_t hi[NT][2], lo[NT][2];
-  float sv[2] = {1.f, 1.f}, ks[2] = {cs, cs}, kt[2] = {1.f, 1.f};
-  if constexpr (I4) {
+}
+
+// Weights of a tile as the value MMAs' operand: bf16 hi + lo of [w s_v, w t s_v].
+template <bool I4, int D, int G>
+struct Weights {
+  uint32_t hi[Tile<I4, D>::kKeys / 16][(G + 3) / 4][2], lo[Tile<I4, D>::kKeys / 16][(G + 3) / 4][2];
+};
+
+template <bool I4, int D, int G, bool W>
+__device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4, D, G>& wt, const Scores<I4, D, G>& sco,
+                                           uint32_t stage, const Query<D, (G + 3) / 4>& q,
+                                           float* __restrict__ scores, int j0, int n, int lane) {
+  using T = Tile<I4, D>;
+  using Sc = Scores<I4, D, G>;
+  constexpr int NT = Sc::NT, NB = Sc::NB, KS = D / 16;
+  const int g = lane >> 2, t = lane & 3;
+  float sc[NB][NT][2], tt[NB][NT][2], sv[NB][2];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      sv[r] = bf_lo(lds32(stage + T::kPOff + 4 * (T::kKeys + kb + g + 8 * r)));
-      kt[r] = bf_lo(pk[r]) * 64.f;
-      ks[r] = kt[r] * cs;
-    }
-  }
-  float sc[NT][2], tt[NT][2];
-  bool raise = false;
+      const int key = 16 * b + g + 8 * r;
+      uint32_t pk = 0u, pv = 0u;
+      if constexpr (I4) lds64(pk, pv, stage + T::kPOff + 8 * key);
+      sv[b][r] = I4 ? bf_lo(pv) : 1.f;
 #pragma unroll
-  for (int u = 0; u < NT; ++u) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int j = j0 + kb + g + 8 * r;
-      const bool seen = j < n;
-      sc[u][r] = seen ? (S[u][0][2 * r] + S[u][1][2 * r]) * ks[r] : -CUDART_INF_F;
-      tt[u][r] = (S[u][0][2 * r + 1] + S[u][1][2 * r + 1]) * kt[r];
-      if constexpr (W) {
-        if (seen && t < G) scores[(size_t)j * G + 4 * u + t] = sc[u][r];
+      for (int u = 0; u < NT; ++u) {
+        float s1 = sco.S[b][u][0][2 * r], s2 = sco.S[b][u][0][2 * r + 1];
+        if constexpr (Sc::NC == 2) {
+          s1 += sco.S[b][u][1][2 * r];
+          s2 += sco.S[b][u][1][2 * r + 1];
+        }
+        if constexpr (I4) {  // sums of raw codes: the zero point times the row's sum goes off
+          const float z = bf_hi(pk), sk = bf_lo(pk);
+          s1 = fmaf(-z, q.sum[u][0], s1) * (q.scale[u][0] * sk);
+          s2 = fmaf(-z, q.sum[u][1], s2) * sk;  // its power of two comes in write_records
+        } else {
+          s1 *= q.cs;
+        }
+        sc[b][u][r] = s1;
+        tt[b][u][r] = s2;
+        if constexpr (W) {
+          if (j0 + key < n && t < G) scores[(size_t)(j0 + key) * G + 4 * u + t] = s1;
+        }
       }
     }
-    raise |= fmaxf(sc[u][0], sc[u][1]) > s.m[u];
+  if (j0 + T::kKeys > n) {  // keys behind the end
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (j0 + 16 * b + g + 8 * r >= n) sc[b][u][r] = -CUDART_INF_F;
   }
+  bool raise = false;
+#pragma unroll
+  for (int u = 0; u < NT; ++u)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) raise |= sc[b][u][0] > s.m[u] || sc[b][u][1] > s.m[u];
   if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      float mx = fmaxf(sc[u][0], sc[u][1]);
+      float mx = sc[0][u][0];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1]));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float m = mx > s.m[u] ? mx + kHeadroom : s.m[u];
-      const float f = exp2f(s.m[u] - m);
+      const float f = ex2(s.m[u] - m);
       s.m[u] = m;
       s.omega[u] *= f;
       s.T[u] *= f;
@@ -298,27 +504,44 @@ __device__ __forceinline__ void compute_block(State<D, (G + 3) / 4>& s, uint32_t
     }
   }
 #pragma unroll
-  for (int u = 0; u < NT; ++u) {
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const float w = exp2f(sc[u][r] - s.m[u]);
-      const float wt = w * tt[u][r];
-      s.omega[u] += w;
-      s.T[u] += wt;
-      const float p0 = w * sv[r], p1 = wt * sv[r];
-      const uint32_t h = pack_bf16(p0, p1);
-      const uint32_t l = pack_bf16(p0 - bf_lo(h), p1 - bf_hi(h));
-      if constexpr (G == 1) {
-        hi[u][r] = movmatrix_trans(t == 0 ? h : (t == 1 ? l : 0u));
-      } else if constexpr (G == 2) {
-        hi[u][r] = movmatrix_trans(t < 2 ? h : l);
-      } else {
-        hi[u][r] = movmatrix_trans(h);
-        lo[u][r] = movmatrix_trans(l);
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        const float w = ex2(sc[b][u][r] - s.m[u]);
+        const float w_t = w * tt[b][u][r];
+        s.omega[u] += w;
+        s.T[u] += w_t;
+        const float p0 = I4 ? w * sv[b][r] : w, p1 = I4 ? w_t * sv[b][r] : w_t;
+        const uint32_t h = pack_bf16(p0, p1);
+        const uint32_t l = pack_bf16(p0 - bf_lo(h), p1 - bf_hi(h));
+        if constexpr (G == 1) {
+          wt.hi[b][u][r] = movmatrix_trans((t & 1) ? l : h);  // columns 4..7 repeat 0..3, unused
+        } else if constexpr (G == 2) {
+          wt.hi[b][u][r] = movmatrix_trans(t < 2 ? h : l);
+        } else {
+          wt.hi[b][u][r] = movmatrix_trans(h);
+          wt.lo[b][u][r] = movmatrix_trans(l);
+        }
       }
     }
-  }
-  // ---- values: rows = head dims, contraction over the block's 16 keys.
+}
+
+// Values of block b: rows = head dims, contraction over the 16 keys.
+template <bool I4, int D, int G>
+__device__ __forceinline__ void value_block(State<D, (G + 3) / 4>& s, const Weights<I4, D, G>& wt, uint32_t stage, int b,
+                                            int lane) {
+  using T = Tile<I4, D>;
+  constexpr int NT = (G + 3) / 4, KS = D / 16;
+  const int g = lane >> 2, t = lane & 3;
+  auto mma = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+    for (int u = 0; u < NT; ++u) {
+      mma_bf16(s.O[u][mt], a0, a1, a2, a3, wt.hi[b][u][0], wt.hi[b][u][1]);
+      if constexpr (G >= 4) mma_bf16(s.O[u][mt], a0, a1, a2, a3, wt.lo[b][u][0], wt.lo[b][u][1]);
+    }
+  };
   if constexpr (I4) {
     constexpr int WPG = D / 64;  // code words a lane has of a key
     uint32_t w[4][2], mz[2];
@@ -326,7 +549,7 @@ __device__ __forceinline__ void compute_block(State<D, (G + 3) / 4>& s, uint32_t
     for (int e = 0; e < 4; ++e) {
       // Key 2t + (e & 1) + 8 (e >> 1); its slot (v_place) is 8 (e >> 1) + 4 (e & 1) + t.
       const int slot = 8 * (e >> 1) + 4 * (e & 1) + t;
-      const uint32_t row = stage + T::kVOff + (kb + slot) * T::kRow;
+      const uint32_t row = stage + T::kVOff + (16 * b + slot) * T::kRow;
       if constexpr (WPG == 2) {
         lds64(w[e][0], w[e][1], row + ((8 * g) ^ ((slot & 2) << 4)));
       } else {
@@ -335,12 +558,12 @@ __device__ __forceinline__ void compute_block(State<D, (G + 3) / 4>& s, uint32_t
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t pa, pb;
-      lds64(pa, pb, stage + T::kPOff + 4 * (T::kKeys + kb + 2 * t + 8 * e));
-      mz[e] = neg_zero_points(__byte_perm(pa, pb, 0x7632));
+      uint32_t kv[4];  // (K word, V word) of two keys
+      lds128(kv, stage + T::kPOff + 8 * (16 * b + 2 * t + 8 * e));
+      mz[e] = neg_zero_points(__byte_perm(kv[1], kv[3], 0x7632));
     }
 #pragma unroll
-    for (int i = 0; i < WPG; ++i) {
+    for (int i = 0; i < WPG; ++i)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const uint32_t sel = half ? 0x7632 : 0x5410;
@@ -348,29 +571,17 @@ __device__ __forceinline__ void compute_block(State<D, (G + 3) / 4>& s, uint32_t
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
           const uint32_t x8 = p ? x >> 8 : x, y8 = p ? y >> 8 : y;
-          const uint32_t a0 = nib_even(x8, mz[0]), a1 = nib_odd(x8, mz[0]);
-          const uint32_t a2 = nib_even(y8, mz[1]), a3 = nib_odd(y8, mz[1]);
-          const int mt = 4 * i + 2 * half + p;
-#pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            mma_bf16(s.O[u][mt], a0, a1, a2, a3, hi[u][0], hi[u][1]);
-            if constexpr (G >= 4) mma_bf16(s.O[u][mt], a0, a1, a2, a3, lo[u][0], lo[u][1]);
-          }
+          mma(4 * i + 2 * half + p, nib_even(x8, mz[0]), nib_odd(x8, mz[0]), nib_even(y8, mz[1]), nib_odd(y8, mz[1]));
         }
       }
-    }
   } else {
     // Matrices of ldmatrix: (dims 0-7 | 8-15 of the tile) x (keys 0-7 | 8-15).
-    const int key = kb + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+    const int key = 16 * b + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) {
       uint32_t x[4];
       ldmatrix4_trans(x, stage + T::kVOff + v_place<I4, D>(key, 2 * mt + half));
-#pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        mma_bf16(s.O[u][mt], x[0], x[1], x[2], x[3], hi[u][0], hi[u][1]);
-        if constexpr (G >= 4) mma_bf16(s.O[u][mt], x[0], x[1], x[2], x[3], lo[u][0], lo[u][1]);
-      }
+      mma(mt, x[0], x[1], x[2], x[3]);
     }
   }
 }
@@ -379,96 +590,17 @@ __device__ __forceinline__ void compute_block(State<D, (G + 3) / 4>& s, uint32_t
 template <int D>
 constexpr int kRec = 2 * D + 4;
 
-template <bool I4, int D, int G, bool W>
-__global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(const CacheDecodeArgs a) {
-  using T = Tile<I4, D>;
-  constexpr int NT = (G + 3) / 4, KS = D / 16, R = kRec<D>;
-  static_assert((kWarps + 1) * G * R * 4 <= T::kSmem, "the merge reuses the ring");
-  extern __shared__ __align__(128) char smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The warp's state as G records.
+template <bool I4, int D, int G>
+__device__ __forceinline__ void write_records(State<D, (G + 3) / 4>& s, const Query<D, (G + 3) / 4>& q, float* recs,
+                                              int lane) {
+  constexpr int KS = D / 16, R = kRec<D>;
   const int g = lane >> 2, t = lane & 3;
-  const int unit = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  grid_dep_wait();
-  grid_dep_launch();
-  const int n = a.seqlens[unit / a.Hkv];
-  const size_t head0 = (size_t)unit * G;  // first query row of the group ([B, H, d] with H = Hkv G)
-  if (n < 1 || n > a.L) {                 // the same for every CTA of the unit
-    if (split == 0) {
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head0 * D;
-      for (int e = threadIdx.x; e < G * D; e += kThreads) out[e] = __float2bfloat16(0.f);
-      if (threadIdx.x == 0) atomicOr(a.status, kStatusBadSeqlen);
-    }
-    return;
-  }
-  const size_t row0 = (size_t)unit * a.L;
-  const int tiles = (n + T::kKeys - 1) / T::kKeys;
-  const int tile0 = (int)((long long)tiles * split / a.splits) + warp;
-  const int tile1 = (int)((long long)tiles * (split + 1) / a.splits);
-  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * T::kWarpBytes;
-  // ---- fill the ring.
+  constexpr float kUnit = I4 ? 64.f : 1.f;  // (c - z) 2^-6
 #pragma unroll
-  for (int i = 0; i < T::kStages - 1; ++i) {
-    const int tile = tile0 + i * kWarps;
-    if (tile < tile1) load_tile<I4, D>(ring + i * T::kBytes, a, row0, tile * T::kKeys, n, lane);
-    cp_commit();
-  }
-  // ---- query rows as MMA columns: column g is q (even) or rho (odd) of head g/2 (modulo G).
-  uint32_t qf[NT][KS][2];
-#pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    const int h = (G >= 4) ? 4 * u + (g >> 1) : (g >> 1) % G;
-    const uint4* row =
-        reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>((g & 1) ? a.r : a.q) + (head0 + h) * D);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      if constexpr (I4) {
-        const uint4 v = row[(D / 32) * t + i];  // the eight dims of one code word
-        qf[u][2 * i][0] = __byte_perm(v.x, v.z, 0x5410);
-        qf[u][2 * i][1] = __byte_perm(v.x, v.z, 0x7632);
-        qf[u][2 * i + 1][0] = __byte_perm(v.y, v.w, 0x5410);
-        qf[u][2 * i + 1][1] = __byte_perm(v.y, v.w, 0x7632);
-      } else {
-        const uint4 v = row[4 * i + t];
-        qf[u][2 * i][0] = v.x;
-        qf[u][2 * i][1] = v.y;
-        qf[u][2 * i + 1][0] = v.z;
-        qf[u][2 * i + 1][1] = v.w;
-      }
-    }
-  }
-  const float cs = kLog2e * rsqrtf((float)D);
-  State<D, NT> s;
-#pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    s.m[u] = kNoRef;
-    s.omega[u] = s.T[u] = 0.f;
-#pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s.O[u][i][e] = 0.f;
-  }
-  float* scores = W ? a.scores + row0 * G : nullptr;
-  int stage = 0;
-  for (int tile = tile0; tile < tile1; tile += kWarps) {
-    cp_wait<T::kStages - 2>();
-    __syncwarp();  // every lane's copies have landed, and the stage refilled below is no longer read
-    const int next = tile + (T::kStages - 1) * kWarps;
-    const int fill = stage == 0 ? T::kStages - 1 : stage - 1;
-    if (next < tile1) load_tile<I4, D>(ring + fill * T::kBytes, a, row0, next * T::kKeys, n, lane);
-    cp_commit();
-#pragma unroll
-    for (int blk = 0; blk < T::kKeys / 16; ++blk)
-      compute_block<I4, D, G, W>(s, ring + stage * T::kBytes, blk, qf, cs, scores, tile * T::kKeys, n, lane);
-    stage = stage == T::kStages - 1 ? 0 : stage + 1;
-  }
-  // ---- merge the warps: records in shared memory, over the ring.
-  cp_wait<0>();
-  __syncthreads();
-  float* recs = reinterpret_cast<float*>(smem);        // [warp][G][R]
-  float* merged = recs + kWarps * G * R;               // [G][R]
-  constexpr float kUnit = I4 ? 64.f : 1.f;             // (c - z) 2^-6
-#pragma unroll
-  for (int u = 0; u < NT; ++u) {
+  for (int u = 0; u < (G + 3) / 4; ++u) {
+    const float f2 = I4 ? q.scale[u][1] : 1.f;  // of what holds t
+    s.T[u] *= f2;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       s.omega[u] += __shfl_xor_sync(0xffffffffu, s.omega[u], o);
@@ -481,27 +613,286 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
         for (int e = 0; e < 4; ++e) s.O[u][i][e] += __shfl_xor_sync(0xffffffffu, s.O[u][i][e], G);
     }
     if (t < G) {
-      float* rec = recs + (warp * G + 4 * u + t) * R;
-      if (g == 0) {
-        rec[0] = s.m[u];
-        rec[1] = s.omega[u];
-        rec[2] = s.T[u];
-      }
+      float* rec = recs + (4 * u + t) * R;
+      if (g == 0) *reinterpret_cast<float4*>(rec) = make_float4(s.m[u], s.omega[u], s.T[u], 0.f);
+      if constexpr (I4) {  // a lane's dims are D / 8 neighbours
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const int d0 = I4 ? 8 * ((D / 64) * g + (i >> 2)) + 2 * (i & 3) : 16 * i + g;
-        const int d1 = I4 ? d0 + 1 : d0 + 8;
-        rec[4 + d0] = s.O[u][i][0] * kUnit;
-        rec[4 + D + d0] = s.O[u][i][1] * kUnit;
-        rec[4 + d1] = s.O[u][i][2] * kUnit;
-        rec[4 + D + d1] = s.O[u][i][3] * kUnit;
+        for (int i = 0; i < KS; i += 2) {
+          const int d0 = (D / 8) * g + 2 * i;
+          const float(&x)[4] = s.O[u][i];
+          const float(&y)[4] = s.O[u][i + 1];
+          *reinterpret_cast<float4*>(rec + 4 + d0) =
+              make_float4(x[0] * kUnit, x[2] * kUnit, y[0] * kUnit, y[2] * kUnit);
+          *reinterpret_cast<float4*>(rec + 4 + D + d0) =
+              make_float4(x[1] * (kUnit * f2), x[3] * (kUnit * f2), y[1] * (kUnit * f2), y[3] * (kUnit * f2));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          const int d0 = 16 * i + g;
+          rec[4 + d0] = s.O[u][i][0];
+          rec[4 + D + d0] = s.O[u][i][1];
+          rec[4 + d0 + 8] = s.O[u][i][2];
+          rec[4 + D + d0 + 8] = s.O[u][i][3];
+        }
       }
     }
   }
+}
+
+__device__ __forceinline__ bool bad_len(int n, int L) { return n < 1 || n > L; }
+
+// Zeros for all heads of a sequence whose length is not in 1..L.
+__device__ void zero_sequence(const CacheDecodeArgs& a, int b, int first, int step) {
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)b * a.H * a.d;
+  for (int e = first; e < a.H * a.d; e += step) out[e] = __float2bfloat16(0.f);
+  if (first == 0) atomicOr(a.status, kStatusBadSeqlen);
+}
+
+// The tiles of all (b, KV head) in one row of T, cut into P shares that differ by
+// one tile at most, the larger ones first.
+struct Shares {
+  int size, more;  // shares 0 .. more - 1 have size + 1 tiles
+  __device__ __forceinline__ Shares(int T, int P) : size(T / P), more(T % P) {}
+  __device__ __forceinline__ int begin(int c) const { return c * size + min(c, more); }
+  __device__ __forceinline__ int of(int x) const {  // the share of tile x
+    const int y = x - more * (size + 1);
+    return y < 0 ? x / (size + 1) : more + y / size;
+  }
+};
+
+// One warp a share, with no barrier between the warps after the prologue.  The
+// part of (b, KV head) u that begins it goes to record slot u, the part that
+// share c begins with inside of one to slot B Hkv + c.  A warp's ring runs on
+// over the end of a (b, KV head).
+template <bool I4, int D, int G, bool W>
+__global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_flat_kernel(const CacheDecodeArgs a) {
+  using T = Tile<I4, D>;
+  constexpr int NT = (G + 3) / 4, R = kRec<D>, kKeys = T::kKeys;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ int s_sum[kWarps], s_b[kWarps], s_begin[kWarps], s_n[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int P = a.shares;
+  grid_dep_wait();
+  grid_dep_launch();
+  // ---- T, and the sequences that hold the warps' first tiles.
+  int total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int x = 0, n = 0;
+      if (b < a.B) {
+        n = a.seqlens[b];
+        if (!bad_len(n, a.L)) {
+          x = (n + kKeys - 1) / kKeys * a.Hkv;
+        } else if (pass == 0 && b % gridDim.x == blockIdx.x) {
+          zero_sequence(a, b, 0, 1);
+        }
+      }
+      int incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      int before = base;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        base += s_sum[w];
+      }
+      const int excl = before + incl - x;
+      if (a.B <= kThreads) total = base;  // one turn: the sum is known already
+      if ((pass == 1 || a.B <= kThreads) && b < a.B) {
+        const Shares shares(total, P);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const int begin = shares.begin(blockIdx.x * kWarps + w);
+          if (excl <= begin && begin < excl + x) {
+            s_b[w] = b;
+            s_begin[w] = excl;
+            s_n[w] = n;
+          }
+        }
+        if (x == 0 && b % gridDim.x == blockIdx.x)
+          for (int h = 0; h < a.Hkv; ++h) a.parts[b * a.Hkv + h] = make_int2(-1, -1);
+      }
+      __syncthreads();
+    }
+    total = base;
+    if (a.B <= kThreads) break;
+  }
+  const Shares shares(total, P);
+  const int c = blockIdx.x * kWarps + warp;
+  const int begin = shares.begin(c), end = shares.begin(c + 1);
+  if (begin >= end) return;
+  // ---- two cursors, the copies' ahead of the MMAs'.
+  struct Cursor {
+    int b, h, n, tiles, tile;  // sequence, KV head, its length and tiles, the tile
+    __device__ __forceinline__ void next_unit(const CacheDecodeArgs& a) {
+      tile = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        do n = a.seqlens[++b];
+        while (bad_len(n, a.L));
+        tiles = (n + kKeys - 1) / kKeys;
+      }
+    }
+  };
+  Cursor at;
+  at.b = s_b[warp];
+  at.n = s_n[warp];
+  at.tiles = (at.n + kKeys - 1) / kKeys;
+  at.h = (begin - s_begin[warp]) / at.tiles;
+  at.tile = begin - s_begin[warp] - at.h * at.tiles;
+  Cursor ld = at;
+  const Loader<I4, D> loader(lane);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * T::kWarpBytes;
+  int ahead = begin;  // next tile to copy
+  auto copy_next = [&](uint32_t stage) {
+    if (ahead < end) {
+      if (ld.tile == ld.tiles) ld.next_unit(a);
+      loader.copy(a, stage, (ld.b * a.Hkv + ld.h) * a.L + ld.tile * kKeys, ld.n - ld.tile * kKeys,
+                  lane);
+      ++ld.tile;
+      ++ahead;
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < T::kStages - 1; ++i) copy_next(ring + i * T::kBytes);
+  Query<D, NT> q;
+  q.cs = kLog2e * rsqrtf((float)D);
+  State<D, NT> s;
+  int unit = at.b * a.Hkv + at.h;
+  begin_unit<I4, D, G>(a, q, s, unit, lane);
+  // The first share of a (b, KV head) notes where its records are: shares c to the
+  // one of its last tile.  No share between them is empty: with more shares than
+  // tiles the first T have one tile each.
+  auto note = [&](int x) {
+    if (lane == 0) a.parts[unit] = make_int2(c, x + at.tiles <= end ? c : shares.of(x + at.tiles - 1));
+  };
+  int slot = a.B * a.Hkv + c;
+  if (at.tile == 0) {
+    slot = unit;
+    note(begin);
+  }
+  Scores<I4, D, G> sc;
+  Weights<I4, D, G> wt;
+  uint32_t now = ring;
+  cp_wait<T::kStages - 2>();
+  __syncwarp();
+#pragma unroll
+  for (int b = 0; b < kKeys / 16; ++b) score_block<I4, D, G>(sc, now, q, b, lane);
+  for (int x = begin;;) {
+    weigh_tile<I4, D, G, W>(s, wt, sc, now, q, W ? a.scores + (size_t)unit * a.L * G : nullptr, at.tile * kKeys, at.n,
+                            lane);
+    cp_wait<T::kStages - 3>();
+    __syncwarp();  // every lane's copies have landed, and the stage refilled below is no longer read
+    const uint32_t after = now == ring + (T::kStages - 1) * T::kBytes ? ring : now + T::kBytes;
+    copy_next(now == ring ? ring + (T::kStages - 1) * T::kBytes : now - T::kBytes);
+    ++x;
+    if (++at.tile < at.tiles && x < end) {
+      // The value MMAs beside the next tile's score MMAs.
+#pragma unroll
+      for (int b = 0; b < kKeys / 16; ++b) {
+        score_block<I4, D, G>(sc, after, q, b, lane);
+        value_block<I4, D, G>(s, wt, now, b, lane);
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < kKeys / 16; ++b) value_block<I4, D, G>(s, wt, now, b, lane);
+      write_records<I4, D, G>(s, q, a.records + (size_t)slot * G * R, lane);
+      if (x == end) break;
+      at.next_unit(a);
+      slot = unit = at.b * a.Hkv + at.h;
+      note(x);
+      begin_unit<I4, D, G>(a, q, s, unit, lane);
+#pragma unroll
+      for (int b = 0; b < kKeys / 16; ++b) score_block<I4, D, G>(sc, after, q, b, lane);
+    }
+    now = after;
+  }
+  cp_wait<0>();
+}
+
+// Shared memory of a CTA of the next kernel: the rings, and over them at the end
+// a record for each warp and head and the merged ones.
+template <bool I4, int D, int G>
+constexpr int kSmem = Tile<I4, D>::kRing > (kWarps + 1) * G * kRec<D> * 4 ? Tile<I4, D>::kRing
+                                                                        : (kWarps + 1) * G * kRec<D> * 4;
+
+// One (b, KV head) a CTA, or a cluster of `splits` CTAs that cut its keys evenly
+// and merge through distributed shared memory.  The warps take tiles in turn.
+template <bool I4, int D, int G, bool W>
+__global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(const CacheDecodeArgs a) {
+  using T = Tile<I4, D>;
+  constexpr int NT = (G + 3) / 4, R = kRec<D>, kKeys = T::kKeys;
+  extern __shared__ __align__(128) char smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int unit = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int n = a.seqlens[unit / a.Hkv];
+  if (bad_len(n, a.L)) {  // the same for every CTA of the cluster
+    if (split == 0 && unit % a.Hkv == 0) zero_sequence(a, unit / a.Hkv, threadIdx.x, kThreads);
+    return;
+  }
+  const int tiles = (n + kKeys - 1) / kKeys;
+  const int tile0 = (int)((long long)tiles * split / a.splits) + warp;
+  const int tile1 = (int)((long long)tiles * (split + 1) / a.splits);
+  const int row0 = unit * a.L;
+  const Loader<I4, D> loader(lane);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * T::kWarpBytes;
+#pragma unroll
+  for (int i = 0; i < T::kStages - 1; ++i) {
+    const int tile = tile0 + i * kWarps;
+    if (tile < tile1) loader.copy(a, ring + i * T::kBytes, row0 + tile * kKeys, n - tile * kKeys, lane);
+    cp_commit();
+  }
+  Query<D, NT> q;
+  q.cs = kLog2e * rsqrtf((float)D);
+  State<D, NT> s;
+  begin_unit<I4, D, G>(a, q, s, unit, lane);
+  Scores<I4, D, G> sc;
+  Weights<I4, D, G> wt;
+  float* scores = W ? a.scores + (size_t)unit * a.L * G : nullptr;
+  uint32_t now = ring;
+  if (tile0 < tile1) {
+    cp_wait<T::kStages - 2>();
+    __syncwarp();
+#pragma unroll
+    for (int b = 0; b < kKeys / 16; ++b) score_block<I4, D, G>(sc, now, q, b, lane);
+  }
+  // Each turn weighs a tile, then runs its value MMAs beside the next tile's
+  // score MMAs (of a tile behind the last: of whatever the stage holds, unused).
+  for (int tile = tile0; tile < tile1; tile += kWarps) {
+    weigh_tile<I4, D, G, W>(s, wt, sc, now, q, scores, tile * kKeys, n, lane);
+    cp_wait<T::kStages - 3>();
+    __syncwarp();  // every lane's copies have landed, and the stage refilled below is no longer read
+    const uint32_t after = now == ring + (T::kStages - 1) * T::kBytes ? ring : now + T::kBytes;
+    const uint32_t fill = now == ring ? ring + (T::kStages - 1) * T::kBytes : now - T::kBytes;
+    const int next = tile + (T::kStages - 1) * kWarps;
+    if (next < tile1) loader.copy(a, fill, row0 + next * kKeys, n - next * kKeys, lane);
+    cp_commit();
+#pragma unroll
+    for (int b = 0; b < kKeys / 16; ++b) {
+      score_block<I4, D, G>(sc, after, q, b, lane);
+      value_block<I4, D, G>(s, wt, now, b, lane);
+    }
+    now = after;
+  }
+  // ---- merge the warps.
+  cp_wait<0>();
   __syncthreads();
-  const bool final_here = !W && a.splits == 1;
-  float* dst = a.partials ? a.partials + ((size_t)unit * a.splits + split) * G * R : merged;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + head0 * D;
+  float* recs = reinterpret_cast<float*>(smem);  // [warp][G][R], then the merged [G][R]
+  float* merged = recs + kWarps * G * R;
+  write_records<I4, D, G>(s, q, recs + warp * G * R, lane);
+  __syncthreads();
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)unit * G * D;
   for (int e = threadIdx.x; e < G * D; e += kThreads) {
     const int h = e / D, dim = e % D;
     float m = recs[h * R];
@@ -511,17 +902,18 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float* rec = recs + (w * G + h) * R;
-      const float f = exp2f(rec[0] - m);
+      const float f = ex2(rec[0] - m);
       omega += f * rec[1];
       tsum += f * rec[2];
       o1 += f * rec[4 + dim];
       o2 += f * rec[4 + D + dim];
     }
-    if (final_here) {
+    if (a.splits == 1) {
       const float inv = 1.f / omega;
       out[e] = __float2bfloat16(((1.f + tsum * inv) * o1 - o2) * inv);
+      if (W && dim == 0) a.stats[(size_t)unit * G + h] = make_float2(m, omega);
     } else {
-      float* rec = dst + h * R;
+      float* rec = merged + h * R;
       if (dim == 0) {
         rec[0] = m;
         rec[1] = omega;
@@ -531,8 +923,7 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
       rec[4 + D + dim] = o2;
     }
   }
-  if (a.partials || final_here) return;
-  // ---- merge the cluster's CTAs, a share of the outputs each.
+  if (a.splits == 1) return;
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   for (int e = split * kThreads + threadIdx.x; e < G * D; e += a.splits * kThreads) {
@@ -542,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
     float omega = 0.f, tsum = 0.f, o1 = 0.f, o2 = 0.f;
     for (int c = 0; c < a.splits; ++c) {
       const float* rec = cluster.map_shared_rank(merged, c) + h * R;
-      const float f = exp2f(rec[0] - m);
+      const float f = ex2(rec[0] - m);
       omega += f * rec[1];
       tsum += f * rec[2];
       o1 += f * rec[4 + dim];
@@ -554,78 +945,151 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
-constexpr int kFinThreads = 256;
-constexpr int kFinKeys = 1024;  // keys of a CTA of the second kernel
+// The records of (b, KV head) `unit` after a decode in shares: slot `unit` (by
+// share c0), then slot `units + c` of the shares c in (c0, c1].
+struct Parts {
+  int unit, units, c0, c1;
+  __device__ __forceinline__ Parts(const CacheDecodeArgs& a, int u) : unit(u), units(a.B * a.Hkv) {
+    const int2 x = a.parts[u];  // (-1, -1): a sequence of bad length
+    c0 = x.x;
+    c1 = x.y;
+  }
+  __device__ __forceinline__ int slot(int c) const { return c == c0 ? unit : units + c; }
+};
 
-// Merges the records of a unit (the CTA of its first keys writes the output)
-// and turns scores into weights: w_out = w_in + sum_h 2^(s_h - m_h) / omega_h.
-template <int D, int G, bool W>
-__global__ void __launch_bounds__(kFinThreads) cache_finish_kernel(const CacheDecodeArgs a, int parts) {
-  constexpr int R = kRec<D>;
-  __shared__ float sm[G], sinv[G], stb[G];
+// Output of one head from its records, by all threads of a CTA: four dims a
+// lane, the records over groups of D / 4 lanes, each with its own running m.
+template <int D, int G, int kT>
+__device__ __forceinline__ void merge_output(const CacheDecodeArgs& a, const Parts& p, int h, float4 (*acc)[kT],
+                                             float4* head) {
+  constexpr int R = kRec<D>, kLanes = D / 4, kGroups = kT / kLanes;
+  const int dl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+  float4 o1 = make_float4(0.f, 0.f, 0.f, 0.f), o2 = o1;
+  float m = kNoRef, omega = 0.f, tsum = 0.f;
+#pragma unroll 4
+  for (int c = p.c0 + grp; c <= p.c1; c += kGroups) {
+    const float4* rec = reinterpret_cast<const float4*>(a.records + ((size_t)p.slot(c) * G + h) * R);
+    const float4 x = rec[0], y1 = rec[1 + dl], y2 = rec[1 + kLanes + dl];
+    const float top = fmaxf(m, x.x), f0 = ex2(m - top), f = ex2(x.x - top);
+    m = top;
+    omega = f0 * omega + f * x.y;
+    tsum = f0 * tsum + f * x.z;
+    o1.x = f0 * o1.x + f * y1.x, o1.y = f0 * o1.y + f * y1.y, o1.z = f0 * o1.z + f * y1.z, o1.w = f0 * o1.w + f * y1.w;
+    o2.x = f0 * o2.x + f * y2.x, o2.y = f0 * o2.y + f * y2.y, o2.z = f0 * o2.z + f * y2.z, o2.w = f0 * o2.w + f * y2.w;
+  }
+  acc[0][threadIdx.x] = o1;
+  acc[1][threadIdx.x] = o2;
+  if (dl == 0) head[grp] = make_float4(m, omega, tsum, 0.f);
+  __syncthreads();
+  if (threadIdx.x < D) {
+    m = kNoRef;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) m = fmaxf(m, head[c].x);
+    const float* f1 = reinterpret_cast<const float*>(acc[0]) + threadIdx.x;
+    const float* f2 = reinterpret_cast<const float*>(acc[1]) + threadIdx.x;
+    float x = 0.f, y = 0.f;
+    omega = tsum = 0.f;
+#pragma unroll
+    for (int c = 0; c < kGroups; ++c) {
+      const float f = ex2(head[c].x - m);
+      omega += f * head[c].y;
+      tsum += f * head[c].z;
+      x += f * f1[c * D];
+      y += f * f2[c * D];
+    }
+    const float inv = 1.f / omega;
+    static_cast<__nv_bfloat16*>(a.out)[((size_t)p.unit * G + h) * D + threadIdx.x] =
+        __float2bfloat16(((1.f + tsum * inv) * x - y) * inv);
+  }
+}
+
+// After a decode in shares: CTA (unit, h) merges head h of (b, KV head) `unit`.
+template <int D, int G, int kT>
+__global__ void __launch_bounds__(kT) cache_merge_kernel(const CacheDecodeArgs a) {
+  __shared__ float4 acc[2][kT], head[kT / (D / 4)];
+  grid_dep_wait();
+  grid_dep_launch();
+  const Parts p(a, blockIdx.x / G);
+  if (p.c0 >= 0) merge_output<D, G, kT>(a, p, blockIdx.x % G, acc, head);
+}
+
+constexpr int kFinThreads = 256;
+constexpr int kFinKeys = 1024;  // keys of a CTA of the weights' kernel
+
+// Scores to weights: w_out = w_in + sum_h 2^(s_h - m_h) / omega_h.  After a
+// decode in shares it also merges the outputs: CTA `part` of the `parts` of a
+// (b, KV head) the heads part, part + parts, ...
+template <int D, int G>
+__global__ void __launch_bounds__(kFinThreads) cache_weights_kernel(const CacheDecodeArgs a, int parts) {
+  constexpr int kTurns = kFinKeys / kFinThreads;
+  __shared__ float sm[G], sinv[G];
+  __shared__ float4 acc[2][kFinThreads], head[kFinThreads / (D / 4)];
   const int unit = blockIdx.x / parts, part = blockIdx.x % parts;
   grid_dep_wait();
   grid_dep_launch();
   const int n = a.seqlens[unit / a.Hkv];
-  if (n < 1 || n > a.L || part * kFinKeys >= n) return;
-  const float* recs = a.partials + (size_t)unit * a.splits * G * R;
+  if (bad_len(n, a.L) || (part * kFinKeys >= n && part >= G)) return;
+  // Scores and totals do not wait for the statistics.
+  const size_t row0 = (size_t)unit * a.L + part * kFinKeys;
+  const int here = n - part * kFinKeys;
+  float x[kTurns][G], w[kTurns];
+#pragma unroll
+  for (int i = 0; i < kTurns; ++i) {
+    const int j = i * kFinThreads + threadIdx.x;
+    if (j >= here) continue;
+    const float* sc = a.scores + (row0 + j) * G;
+    if constexpr (G >= 4) {
+#pragma unroll
+      for (int h = 0; h < G; h += 4) *reinterpret_cast<float4*>(x[i] + h) = *reinterpret_cast<const float4*>(sc + h);
+    } else if constexpr (G == 2) {
+      *reinterpret_cast<float2*>(x[i]) = *reinterpret_cast<const float2*>(sc);
+    } else {
+      x[i][0] = sc[0];
+    }
+    w[i] = a.w_in[row0 + j];
+  }
   const int lane = threadIdx.x & 31;
-  for (int h = threadIdx.x >> 5; h < G; h += kFinThreads / 32) {
-    float m = kNoRef;
-    for (int c = lane; c < a.splits; c += 32) m = fmaxf(m, recs[(size_t)(c * G + h) * R]);
+  if (a.shares > 0) {
+    const Parts p(a, unit);
+    for (int h = threadIdx.x >> 5; h < G; h += kFinThreads / 32) {
+      float m = kNoRef, omega = 0.f;
+#pragma unroll 4
+      for (int c = p.c0 + lane; c <= p.c1; c += 32) {
+            const float2 r = *reinterpret_cast<const float2*>(a.records + ((size_t)p.slot(c) * G + h) * kRec<D>);
+        const float top = fmaxf(m, r.x);
+        omega = omega * ex2(m - top) + r.y * ex2(r.x - top);
+        m = top;
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float omega = 0.f, tsum = 0.f;
-    for (int c = lane; c < a.splits; c += 32) {
-      const float* rec = recs + (size_t)(c * G + h) * R;
-      const float f = exp2f(rec[0] - m);
-      omega += f * rec[1];
-      tsum += f * rec[2];
+      for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), omega2 = __shfl_xor_sync(0xffffffffu, omega, o);
+        const float top = fmaxf(m, m2);
+        omega = omega * ex2(m - top) + omega2 * ex2(m2 - top);
+        m = top;
+      }
+      if (lane == 0) {
+        sm[h] = m;
+        sinv[h] = 1.f / omega;
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      omega += __shfl_xor_sync(0xffffffffu, omega, o);
-      tsum += __shfl_xor_sync(0xffffffffu, tsum, o);
+    for (int h = part; h < G; h += parts) {
+      merge_output<D, G, kFinThreads>(a, p, h, acc, head);
+      __syncthreads();
     }
-    if (lane == 0) {
-      sm[h] = m;
-      sinv[h] = 1.f / omega;
-      stb[h] = tsum / omega;
-    }
+  } else if (threadIdx.x < G) {
+    const float2 r = a.stats[(size_t)unit * G + threadIdx.x];
+    sm[threadIdx.x] = r.x;
+    sinv[threadIdx.x] = 1.f / r.y;
   }
   __syncthreads();
-  if (part == 0) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (size_t)unit * G * D;
-    for (int e = threadIdx.x; e < G * D; e += kFinThreads) {
-      const int h = e / D, dim = e % D;
-      float o1 = 0.f, o2 = 0.f;
-      for (int c = 0; c < a.splits; ++c) {
-        const float* rec = recs + (size_t)(c * G + h) * R;
-        const float f = exp2f(rec[0] - sm[h]);
-        o1 += f * rec[4 + dim];
-        o2 += f * rec[4 + D + dim];
-      }
-      out[e] = __float2bfloat16(((1.f + stb[h]) * o1 - o2) * sinv[h]);
-    }
-  }
-  if constexpr (W) {
-    const size_t row0 = (size_t)unit * a.L;
-    const int end = min(n, (part + 1) * kFinKeys);
-    for (int j = part * kFinKeys + threadIdx.x; j < end; j += kFinThreads) {
-      const float* sc = a.scores + (row0 + j) * G;
-      float x[G];
-      if constexpr (G >= 4) {
 #pragma unroll
-        for (int h = 0; h < G; h += 4) *reinterpret_cast<float4*>(x + h) = *reinterpret_cast<const float4*>(sc + h);
-      } else {
+  for (int i = 0; i < kTurns; ++i) {
+    const int j = i * kFinThreads + threadIdx.x;
+    if (j >= here) continue;
+    float p = 0.f;
 #pragma unroll
-        for (int h = 0; h < G; ++h) x[h] = sc[h];
-      }
-      float w = 0.f;
-#pragma unroll
-      for (int h = 0; h < G; ++h) w += exp2f(x[h] - sm[h]) * sinv[h];
-      a.w_out[row0 + j] = a.w_in[row0 + j] + w;
-    }
+    for (int h = 0; h < G; ++h) p += ex2(x[i][h] - sm[h]) * sinv[h];
+    a.w_out[row0 + j] = w[i] + p;
   }
 }
 
@@ -655,16 +1119,23 @@ cudaError_t launch(Kern kern, unsigned grid, unsigned block, size_t smem, int cl
 
 template <bool I4, int D, int G, bool W>
 cudaError_t run(const CacheDecodeArgs& a, cudaStream_t st) {
-  using T = Tile<I4, D>;
-  auto kern = cache_decode_kernel<I4, D, G, W>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
-  if (e != cudaSuccess) return e;
+  const int smem = a.shares > 0 ? Tile<I4, D>::kRing : kSmem<I4, D, G>;
   const unsigned units = (unsigned)a.B * a.Hkv;
-  const int cluster = a.partials ? 1 : a.splits;
-  e = launch(kern, units * a.splits, kThreads, T::kSmem, cluster, st, a);
-  if (e != cudaSuccess || !a.partials) return e;
-  const int parts = W ? (a.L + kFinKeys - 1) / kFinKeys : 1;
-  return launch(cache_finish_kernel<D, G, W>, units * parts, kFinThreads, 0, 1, st, a, parts);
+  auto kern = a.shares > 0 ? cache_decode_flat_kernel<I4, D, G, W> : cache_decode_kernel<I4, D, G, W>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = a.shares > 0 ? launch(kern, a.shares / kWarps, kThreads, smem, 1, st, a)
+                   : launch(kern, units * a.splits, kThreads, smem, a.splits, st, a);
+  if (e != cudaSuccess) return e;
+  if constexpr (W) {
+    const int parts = (a.L + kFinKeys - 1) / kFinKeys;
+    return launch(cache_weights_kernel<D, G>, units * parts, kFinThreads, 0, 1, st, a, parts);
+  } else {
+    if (a.shares == 0) return cudaSuccess;
+    // As many threads as there are records to read at once.
+    return a.shares <= 8 * units ? launch(cache_merge_kernel<D, G, 128>, units * G, 128, 0, 1, st, a)
+                                 : launch(cache_merge_kernel<D, G, 512>, units * G, 512, 0, 1, st, a);
+  }
 }
 
 template <bool I4, bool W>
@@ -686,20 +1157,44 @@ cudaError_t pick(const CacheDecodeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-int cache_decode_splits(long long units, int L, int num_sms, bool weights) {
-  // Two waves of four CTAs an SM, while a CTA keeps a 32-key tile for each of its warps.
-  int s = 1;
-  while (s < 64 && units * s < 8ll * num_sms && (long long)L > 128ll * s) s *= 2;
-  (void)weights;
-  return s;
-}
-
-CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool weights) {
+// How the keys are cut, by sizes alone.  Measured on a B200 with 4-bit rows, d =
+// 128, us with shares / one CTA a (b, KV head) / the best cluster of 2 to 8:
+//   many (b, KV head) balance themselves:  64 x 16 of 4096 keys     113 / 107 / 113
+//   fewer, or ragged, need shares:         64 x 8 of 2048..4096      57 /  64 /  64
+//                                          1 x 8 of 32768            27 / 182 /  33
+//   little work ends soonest in one launch: 8 x 8 of 2048..4096, G=4 23 /  29 /  18
+//                                          1 x 2 of 4096             12 /  30 /  12
+// (G = 4 but for the first; each includes about 8 us of an empty graph launch).
+// Weights take a second launch in any case, so only many units go without shares.
+CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool int4, bool weights) {
   CacheDecodeSpace w;
-  w.splits = cache_decode_splits((long long)B * Hkv, L, num_sms, weights);
-  if (weights || w.splits > 8) w.partials = sizeof(float) * (size_t)B * H * w.splits * (2 * d + 4);
-  if (weights) w.scores = sizeof(float) * (size_t)B * H * L;
-  w.partials = (w.partials + 255) / 256 * 256;
+  const long long units = (long long)B * Hkv, slots = (H / Hkv == 8 ? 3ll : 4ll) * num_sms;
+  const int keys = int4 ? 32 : 2048 / d;
+  const long long tiles = units * ((L + keys - 1) / keys);
+  const long long bytes = units * L * (int4 ? d + 8 : 4 * d);
+  const bool flat = 2 * units < 3 * slots && (weights || bytes > (28ll << 20) || L > 16384);
+  if (!flat && !weights)
+    while (w.splits < 8 && units * w.splits * 2 <= slots && (long long)L > 128ll * w.splits &&
+           (units * w.splits * 2 <= num_sms || (long long)L > 1024ll * w.splits))
+      w.splits *= 2;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  if (flat) {
+    // A tile for every warp, and at most 256 records to merge for a (b, KV head) of L keys.
+    const long long warps = tiles < 256 * units ? tiles : 256 * units;
+    w.shares = kWarps * (int)((warps + kWarps - 1) / kWarps < slots ? (warps + kWarps - 1) / kWarps : slots);
+    w.records = take(sizeof(float) * (size_t)(units + w.shares) * (H / Hkv) * (2 * d + 4));
+    w.parts = take(sizeof(int2) * (size_t)units);
+  }
+  if (weights) {
+    w.stats = take(sizeof(float2) * (size_t)B * H);
+    w.scores = take(sizeof(float) * (size_t)B * H * L);
+  }
+  w.bytes = at;
   return w;
 }
 

@@ -668,18 +668,18 @@ int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams
   return cuda_rc(launch_kv_append_int4(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-static size_t cache_decode_bytes(int B, int H, int Hkv, int L, int d, bool weights) {
+static size_t cache_decode_bytes(int B, int H, int Hkv, int L, int d, bool int4, bool weights) {
   if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0) return 0;
-  const CacheDecodeSpace w = cache_decode_space(B, H, Hkv, L, d, num_sms_or_default(), weights);
-  return w.partials + w.scores;
+  return cache_decode_space(B, H, Hkv, L, d, num_sms_or_default(), int4, weights).bytes;
 }
 
 size_t plx_decode_int4kv_workspace_bytes(int B, int H, int Hkv, int L, int d) {
-  return cache_decode_bytes(B, H, Hkv, L, d, false);
+  return cache_decode_bytes(B, H, Hkv, L, d, true, false);
 }
 
 size_t plx_decode_weights_workspace_bytes(int B, int H, int Hkv, int L, int d) {
-  return cache_decode_bytes(B, H, Hkv, L, d, true);
+  // Either cache's decode.
+  return std::max(cache_decode_bytes(B, H, Hkv, L, d, true, true), cache_decode_bytes(B, H, Hkv, L, d, false, true));
 }
 
 static int cache_decode_impl(const void* q, const void* r, const void* K, const void* Kp, const void* V,
@@ -704,10 +704,11 @@ static int cache_decode_impl(const void* q, const void* r, const void* K, const 
   DeviceCache* dc = nullptr;
   int rc = current_device(&dc);
   if (rc != PLX_OK) return rc;
-  const CacheDecodeSpace need = cache_decode_space(B, H, Hkv, L, d, dc->num_sms, weights);
-  if (need.partials + need.scores > 0) {
-    if (!workspace || workspace_bytes < need.partials + need.scores) return PLX_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PLX_ERR_MISALIGNED;
+  const CacheDecodeSpace need = cache_decode_space(B, H, Hkv, L, d, dc->num_sms, int4, weights);
+  char* ws = static_cast<char*>(workspace);
+  if (need.bytes > 0) {
+    if (!ws || workspace_bytes < need.bytes) return PLX_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) & 255u) return PLX_ERR_MISALIGNED;
   }
   CacheDecodeArgs a{};
   a.q = q;
@@ -726,8 +727,15 @@ static int cache_decode_impl(const void* q, const void* r, const void* K, const 
   a.L = L;
   a.d = d;
   a.splits = need.splits;
-  a.partials = need.partials ? static_cast<float*>(workspace) : nullptr;
-  a.scores = need.scores ? reinterpret_cast<float*>(static_cast<char*>(workspace) + need.partials) : nullptr;
+  a.shares = need.shares;
+  if (need.shares > 0) {
+    a.records = reinterpret_cast<float*>(ws + need.records);
+    a.parts = reinterpret_cast<int2*>(ws + need.parts);
+  }
+  if (weights) {
+    a.stats = reinterpret_cast<float2*>(ws + need.stats);
+    a.scores = reinterpret_cast<float*>(ws + need.scores);
+  }
   a.status = dc->status;
   return cuda_rc(launch_cache_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -228,16 +228,20 @@ struct CacheDecodeArgs {
   const float* w_in;  // [B, Hkv, L]; w_out null: no weights
   float* w_out;
   int B, H, Hkv, L, d;
-  int splits;       // CTAs a (b, KV head)
-  float* partials;  // records [B*Hkv, splits, G, 2d + 4]; null: the splits are a cluster
-  float* scores;    // log2-domain scores [B*Hkv, L, G] (weights only)
+  int splits;     // CTAs (a cluster) a (b, KV head), where shares is 0
+  int shares;     // equal shares of all tiles, one warp each
+  float* records; // [B*Hkv + shares, G, 2d + 4] fp32: m, omega, T, pad, O1[d], O2[d]
+  int2* parts;    // [B*Hkv]: first and last share of every (b, KV head), -1 for a bad length
+  float2* stats;  // [B*H]: m and omega of a head that one CTA finished (weights only)
+  float* scores;  // log2-domain scores [B*Hkv, L, G] (weights only)
   int* status;
 };
 struct CacheDecodeSpace {
-  int splits = 1;
-  size_t partials = 0, scores = 0;  // bytes, the scores behind the partials
+  int splits = 1, shares = 0;
+  size_t records = 0, parts = 0, stats = 0, scores = 0;  // byte offsets in the workspace
+  size_t bytes = 0;
 };
-CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool weights);
+CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool int4, bool weights);
 cudaError_t launch_cache_decode(const CacheDecodeArgs& a, cudaStream_t st);
 
 // Eviction (cache_evict.cu).

@@ -238,7 +238,7 @@ def test_cache_decodes_reject_bad_arguments(lib):
     assert lib.plx_decode_weights(*[A] * 6, A + 64, A, 1, 8, 2, 64, 128, *tail) == -1
     assert lib.plx_decode_int4kv_workspace_bytes(1, 8, 3, 64, 128) == 0
     assert lib.plx_decode_weights_workspace_bytes(1, 8, 2, 64, 128) >= 8 * 64 * 4
-    assert lib.plx_decode_int4kv_workspace_bytes(64, 16, 16, 4096, 128) == 0
+    assert lib.plx_decode_int4kv_workspace_bytes(1, 8, 2, 1000, 128) == 0
     assert lib.plx_decode_int4kv_workspace_bytes(1, 1, 1, 1 << 20, 128) > 0
 
 
