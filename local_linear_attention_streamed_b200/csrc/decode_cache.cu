@@ -51,6 +51,8 @@
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
+#include <atomic>
+
 namespace cg = cooperative_groups;
 
 namespace plx {
@@ -1122,8 +1124,15 @@ cudaError_t run(const CacheDecodeArgs& a, cudaStream_t st) {
   const int smem = a.shares > 0 ? Tile<I4, D>::kRing : kSmem<I4, D, G>;
   const unsigned units = (unsigned)a.B * a.Hkv;
   auto kern = a.shares > 0 ? cache_decode_flat_kernel<I4, D, G, W> : cache_decode_kernel<I4, D, G, W>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  // Once a device and kernel: which devices this one is set up on.
+  static std::atomic<uint64_t> ready[2];
+  std::atomic<uint64_t>& set = ready[a.shares > 0];
+  cudaError_t e = cudaSuccess;
+  if (!(set.load(std::memory_order_acquire) >> a.device & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(1ull << a.device, std::memory_order_release);
+  }
   e = a.shares > 0 ? launch(kern, a.shares / kWarps, kThreads, smem, 1, st, a)
                    : launch(kern, units * a.splits, kThreads, smem, a.splits, st, a);
   if (e != cudaSuccess) return e;

@@ -737,6 +737,7 @@ static int cache_decode_impl(const void* q, const void* r, const void* K, const 
     a.scores = reinterpret_cast<float*>(ws + need.scores);
   }
   a.status = dc->status;
+  a.device = (int)(dc - g_dev);
   return cuda_rc(launch_cache_decode(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

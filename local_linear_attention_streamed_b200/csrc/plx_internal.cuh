@@ -235,6 +235,7 @@ struct CacheDecodeArgs {
   float2* stats;  // [B*H]: m and omega of a head that one CTA finished (weights only)
   float* scores;  // log2-domain scores [B*Hkv, L, G] (weights only)
   int* status;
+  int device;     // ordinal, below 64
 };
 struct CacheDecodeSpace {
   int splits = 1, shares = 0;

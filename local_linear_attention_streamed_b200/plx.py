@@ -446,110 +446,105 @@ def decode_fp8kv(q, r, Kcodes, Kscales, Vcodes, Vscales, seqlens, out=None, work
     return out
 
 
-class _Launch:
-    """Where a call runs: the device all its tensors are on, and the given or that device's current stream.
+def _elsewhere(first, stream):
+    """Context in which a call on the tensor ``first`` has to run: the given stream, or the tensor's device where that
+    is not the current one (so that what is allocated inside may be used at once); None where both are current."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if stream is not None:
+        if stream.device_index != index:
+            raise ValueError(f"the stream is on device {stream.device_index}, the tensors on {index}")
+        return torch.cuda.stream(stream)
+    return None if index == torch.cuda.current_device() else torch.cuda.device(index)
 
-    A context manager: inside it that device and stream are torch's current ones, so that what is
-    allocated there may be used on the stream at once.  ptr() checks a tensor and returns its address."""
 
-    __slots__ = ("device", "stream", "_guards")
+def _ptr(t, name: str, shape, dtype, index: int) -> int:
+    """Address of a contiguous tensor of this shape and type on device ``index``."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def __init__(self, first, stream):
-        if not first.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        self.device = first.device
-        self.stream = stream
-        if stream is not None and stream.device != self.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
 
-    def __enter__(self):
-        self._guards = []
-        if self.stream is not None:
-            self._guards.append(torch.cuda.stream(self.stream))
-        elif self.device.index != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(self.device))
-        for guard in self._guards:
-            guard.__enter__()
-        return self
+def _workspace(given, need: int, index: int):
+    """(tensor that keeps it alive, address, bytes) of the caller's workspace or a new one."""
+    if given is None:
+        if need == 0:
+            return None, None, 0
+        given = torch.empty(need, dtype=torch.uint8, device=index)
+    elif given.get_device() != index or not given.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{index}")
+    return given, given.data_ptr(), given.numel() * given.element_size()
 
-    def __exit__(self, *exc):
-        for guard in reversed(self._guards):
-            guard.__exit__(*exc)
 
-    def ptr(self, t, name: str, shape, dtype) -> int:
-        if t.shape != shape or t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {self.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
-
-    def workspace(self, given, need: int):
-        """(tensor that keeps it alive, address, bytes) of the caller's workspace or a new one."""
-        if given is None:
-            if need == 0:
-                return None, None, 0
-            given = torch.empty(need, dtype=torch.uint8, device=self.device)
-        elif given.device != self.device or not given.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {self.device}")
-        return given, given.data_ptr(), given.numel() * given.element_size()
-
-    def raw_stream(self) -> int:
-        return torch.cuda.current_stream(self.device).cuda_stream
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device, as its address
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def kv_quantize_int4(X, codes=None, params=None, stream=None):
     """4-bit rows of bf16 cache rows X [..., d]: returns (codes uint8 [..., d/2], params bf16 [..., 2]),
     each row standing for scale * (code - zero point) with (scale, zero point) its params."""
-    d = X.shape[-1]
-    lead = X.shape[:-1]
-    with _Launch(X, stream) as on:
-        if codes is None:
-            codes = torch.empty((*lead, d // 2), dtype=torch.uint8, device=X.device)
-        if params is None:
-            params = torch.empty((*lead, 2), dtype=torch.bfloat16, device=X.device)
-        rc = lib.plx_kv_quantize_int4(on.ptr(X, "X", X.shape, torch.bfloat16),
-                                      on.ptr(codes, "codes", (*lead, d // 2), torch.uint8),
-                                      on.ptr(params, "params", (*lead, 2), torch.bfloat16),
-                                      X.numel() // d, d, on.raw_stream())
+    at = _elsewhere(X, stream)
+    if at is not None:
+        with at:
+            return kv_quantize_int4(X, codes, params)
+    index, shape = X.get_device(), X.shape
+    d, lead = shape[-1], shape[:-1]
+    half, pair = (*lead, d // 2), (*lead, 2)
+    if codes is None:
+        codes = torch.empty(half, dtype=_U8, device=index)
+    if params is None:
+        params = torch.empty(pair, dtype=_BF16, device=index)
+    rc = lib.plx_kv_quantize_int4(_ptr(X, "X", shape, _BF16, index), _ptr(codes, "codes", half, _U8, index),
+                                  _ptr(params, "params", pair, _BF16, index), math.prod(lead), d, _raw_stream(index))
     _check(rc, "plx_kv_quantize_int4")
     return codes, params
 
 
 def kv_dequantize_int4(codes, params, out=None, stream=None):
     """The bf16 values [..., d] that 4-bit rows stand for: codes uint8 [..., d/2], params bf16 [..., 2]."""
-    lead, d = codes.shape[:-1], 2 * codes.shape[-1]
-    with _Launch(codes, stream) as on:
-        if out is None:
-            out = torch.empty((*lead, d), dtype=torch.bfloat16, device=codes.device)
-        rc = lib.plx_kv_dequantize_int4(on.ptr(codes, "codes", codes.shape, torch.uint8),
-                                        on.ptr(params, "params", (*lead, 2), torch.bfloat16),
-                                        on.ptr(out, "out", (*lead, d), torch.bfloat16),
-                                        codes.numel() // (d // 2), d, on.raw_stream())
+    at = _elsewhere(codes, stream)
+    if at is not None:
+        with at:
+            return kv_dequantize_int4(codes, params, out)
+    index, shape = codes.get_device(), codes.shape
+    d, lead = 2 * shape[-1], shape[:-1]
+    full = (*lead, d)
+    if out is None:
+        out = torch.empty(full, dtype=_BF16, device=index)
+    rc = lib.plx_kv_dequantize_int4(_ptr(codes, "codes", shape, _U8, index),
+                                    _ptr(params, "params", (*lead, 2), _BF16, index),
+                                    _ptr(out, "out", full, _BF16, index), math.prod(lead), d, _raw_stream(index))
     _check(rc, "plx_kv_dequantize_int4")
     return out
 
 
-def _int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d):
+def _int4_cache(Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d, index):
     rows, words = (B, Hkv, L, d // 2), (B, Hkv, L, 2)
-    return (on.ptr(Kcodes, "Kcodes", rows, torch.uint8), on.ptr(Kparams, "Kparams", words, torch.bfloat16),
-            on.ptr(Vcodes, "Vcodes", rows, torch.uint8), on.ptr(Vparams, "Vparams", words, torch.bfloat16))
+    return (_ptr(Kcodes, "Kcodes", rows, _U8, index), _ptr(Kparams, "Kparams", words, _BF16, index),
+            _ptr(Vcodes, "Vcodes", rows, _U8, index), _ptr(Vparams, "Vparams", words, _BF16, index))
 
 
 def kv_append_int4(k, v, Kcodes, Kparams, Vcodes, Vparams, seqlens, k_out=None, v_out=None, stream=None):
     """Writes the new rows k, v bf16 [B, Hkv, d] to row seqlens - 1 of a 4-bit cache (codes uint8
     [B, Hkv, L, d/2], params bf16 [B, Hkv, L, 2]); k_out, v_out, if given, get the values they stand for."""
-    B, Hkv, d = k.shape
+    at = _elsewhere(k, stream)
+    if at is not None:
+        with at:
+            return kv_append_int4(k, v, Kcodes, Kparams, Vcodes, Vparams, seqlens, k_out, v_out)
+    index, new = k.get_device(), k.shape
+    B, Hkv, d = new
     L = Kcodes.shape[2]
-    new = (B, Hkv, d)
-    with _Launch(k, stream) as on:
-        rc = lib.plx_kv_append_int4(on.ptr(k, "k", new, torch.bfloat16), on.ptr(v, "v", new, torch.bfloat16),
-                                    *_int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d),
-                                    on.ptr(seqlens, "seqlens", (B,), torch.int32),
-                                    None if k_out is None else on.ptr(k_out, "k_out", new, torch.bfloat16),
-                                    None if v_out is None else on.ptr(v_out, "v_out", new, torch.bfloat16),
-                                    B, Hkv, L, d, on.raw_stream())
+    rc = lib.plx_kv_append_int4(_ptr(k, "k", new, _BF16, index), _ptr(v, "v", new, _BF16, index),
+                                *_int4_cache(Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d, index),
+                                _ptr(seqlens, "seqlens", (B,), _I32, index),
+                                None if k_out is None else _ptr(k_out, "k_out", new, _BF16, index),
+                                None if v_out is None else _ptr(v_out, "v_out", new, _BF16, index),
+                                B, Hkv, L, d, _raw_stream(index))
     _check(rc, "plx_kv_append_int4")
 
 
@@ -560,17 +555,20 @@ def decode_int4kv_workspace_bytes(B: int, H: int, Hkv: int, L: int, d: int) -> i
 def decode_int4kv(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, out=None, workspace=None, stream=None):
     """Decode over a 4-bit cache: q, r bf16 [B, H, d]; codes uint8 [B, Hkv, L, d/2]; params bf16
     [B, Hkv, L, 2]; seqlens int32 [B]."""
-    B, H, d = q.shape
-    Hkv, L = Kcodes.shape[1], Kcodes.shape[2]
-    with _Launch(q, stream) as on:
-        if out is None:
-            out = torch.empty_like(q)
-        ws, ws_ptr, ws_bytes = on.workspace(workspace, lib.plx_decode_int4kv_workspace_bytes(B, H, Hkv, L, d))
-        rc = lib.plx_decode_int4kv(on.ptr(q, "q", q.shape, torch.bfloat16), on.ptr(r, "r", q.shape, torch.bfloat16),
-                                   *_int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d),
-                                   on.ptr(seqlens, "seqlens", (B,), torch.int32),
-                                   on.ptr(out, "out", q.shape, torch.bfloat16),
-                                   B, H, Hkv, L, d, ws_ptr, ws_bytes, on.raw_stream())
+    at = _elsewhere(q, stream)
+    if at is not None:
+        with at:
+            return decode_int4kv(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, out, workspace)
+    index, heads = q.get_device(), q.shape
+    B, H, d = heads
+    _, Hkv, L, _ = Kcodes.shape
+    if out is None:
+        out = torch.empty_like(q)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, lib.plx_decode_int4kv_workspace_bytes(B, H, Hkv, L, d), index)
+    rc = lib.plx_decode_int4kv(_ptr(q, "q", heads, _BF16, index), _ptr(r, "r", heads, _BF16, index),
+                               *_int4_cache(Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d, index),
+                               _ptr(seqlens, "seqlens", (B,), _I32, index), _ptr(out, "out", heads, _BF16, index),
+                               B, H, Hkv, L, d, ws_ptr, ws_bytes, _raw_stream(index))
     _check(rc, "plx_decode_int4kv")
     return out
 
@@ -582,24 +580,27 @@ def decode_weights_workspace_bytes(B: int, H: int, Hkv: int, L: int, d: int) -> 
 def decode_weights(q, r, Kcache, Vcache, seqlens, weights, weights_out=None, out=None, workspace=None, stream=None):
     """decode_gqa that also writes weights_out = weights + every visible key's softmax weight, summed over
     the query heads of its KV head (fp32 [B, Hkv, L]; weights itself when None); returns out."""
-    B, Hkv, L, d = Kcache.shape
-    H = q.shape[1]
-    cache, totals = (B, Hkv, L, d), (B, Hkv, L)
-    with _Launch(q, stream) as on:
-        if out is None:
-            out = torch.empty_like(q)
-        if weights_out is None:
-            weights_out = weights
-        ws, ws_ptr, ws_bytes = on.workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d))
-        rc = lib.plx_decode_weights(on.ptr(q, "q", (B, H, d), torch.bfloat16),
-                                    on.ptr(r, "r", (B, H, d), torch.bfloat16),
-                                    on.ptr(Kcache, "Kcache", cache, torch.bfloat16),
-                                    on.ptr(Vcache, "Vcache", cache, torch.bfloat16),
-                                    on.ptr(seqlens, "seqlens", (B,), torch.int32),
-                                    on.ptr(weights, "weights", totals, torch.float32),
-                                    on.ptr(weights_out, "weights_out", totals, torch.float32),
-                                    on.ptr(out, "out", (B, H, d), torch.bfloat16),
-                                    B, H, Hkv, L, d, ws_ptr, ws_bytes, on.raw_stream())
+    at = _elsewhere(q, stream)
+    if at is not None:
+        with at:
+            return decode_weights(q, r, Kcache, Vcache, seqlens, weights, weights_out, out, workspace)
+    index, heads, cache = q.get_device(), q.shape, Kcache.shape
+    B, Hkv, L, d = cache
+    H = heads[1]
+    heads, totals = (B, H, d), (B, Hkv, L)
+    if out is None:
+        out = torch.empty_like(q)
+    if weights_out is None:
+        weights_out = weights
+    ws, ws_ptr, ws_bytes = _workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d), index)
+    rc = lib.plx_decode_weights(_ptr(q, "q", heads, _BF16, index), _ptr(r, "r", heads, _BF16, index),
+                                _ptr(Kcache, "Kcache", cache, _BF16, index),
+                                _ptr(Vcache, "Vcache", cache, _BF16, index),
+                                _ptr(seqlens, "seqlens", (B,), _I32, index),
+                                _ptr(weights, "weights", totals, _F32, index),
+                                _ptr(weights_out, "weights_out", totals, _F32, index),
+                                _ptr(out, "out", heads, _BF16, index), B, H, Hkv, L, d, ws_ptr, ws_bytes,
+                                _raw_stream(index))
     _check(rc, "plx_decode_weights")
     return out
 
@@ -607,23 +608,27 @@ def decode_weights(q, r, Kcache, Vcache, seqlens, weights, weights_out=None, out
 def decode_int4kv_weights(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, weights, weights_out=None, out=None,
                           workspace=None, stream=None):
     """decode_weights over a 4-bit cache (decode_int4kv)."""
-    B, H, d = q.shape
-    Hkv, L = Kcodes.shape[1], Kcodes.shape[2]
+    at = _elsewhere(q, stream)
+    if at is not None:
+        with at:
+            return decode_int4kv_weights(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, weights, weights_out, out,
+                                         workspace)
+    index, heads = q.get_device(), q.shape
+    B, H, d = heads
+    _, Hkv, L, _ = Kcodes.shape
     totals = (B, Hkv, L)
-    with _Launch(q, stream) as on:
-        if out is None:
-            out = torch.empty_like(q)
-        if weights_out is None:
-            weights_out = weights
-        ws, ws_ptr, ws_bytes = on.workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d))
-        rc = lib.plx_decode_int4kv_weights(on.ptr(q, "q", q.shape, torch.bfloat16),
-                                           on.ptr(r, "r", q.shape, torch.bfloat16),
-                                           *_int4_cache_ptrs(on, Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d),
-                                           on.ptr(seqlens, "seqlens", (B,), torch.int32),
-                                           on.ptr(weights, "weights", totals, torch.float32),
-                                           on.ptr(weights_out, "weights_out", totals, torch.float32),
-                                           on.ptr(out, "out", q.shape, torch.bfloat16),
-                                           B, H, Hkv, L, d, ws_ptr, ws_bytes, on.raw_stream())
+    if out is None:
+        out = torch.empty_like(q)
+    if weights_out is None:
+        weights_out = weights
+    ws, ws_ptr, ws_bytes = _workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d), index)
+    rc = lib.plx_decode_int4kv_weights(_ptr(q, "q", heads, _BF16, index), _ptr(r, "r", heads, _BF16, index),
+                                       *_int4_cache(Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d, index),
+                                       _ptr(seqlens, "seqlens", (B,), _I32, index),
+                                       _ptr(weights, "weights", totals, _F32, index),
+                                       _ptr(weights_out, "weights_out", totals, _F32, index),
+                                       _ptr(out, "out", heads, _BF16, index), B, H, Hkv, L, d, ws_ptr, ws_bytes,
+                                       _raw_stream(index))
     _check(rc, "plx_decode_int4kv_weights")
     return out
 
@@ -638,29 +643,32 @@ def cache_evict(caches, weights, seqlens, budget: int, sinks: int = 0, recent: i
     [B, Hkv, L_out, ...] and weights_out [B, Hkv, L_out] (0 behind the last), L_out >= min(budget, L); both in
     place when None.  Returns (kept int32 [B, Hkv, min(budget, L)], the rows' old positions, -1 behind the
     last; new seqlens int32 [B])."""
-    B, Hkv, L = weights.shape
-    caches = tuple(caches)
-    in_place = caches_out is None
-    if in_place != (weights_out is None):
+    at = _elsewhere(weights, stream)
+    if at is not None:
+        with at:
+            return cache_evict(caches, weights, seqlens, budget, sinks, recent, caches_out, weights_out, seqlens_out)
+    if (caches_out is None) != (weights_out is None):
         raise ValueError("caches_out and weights_out go together: both given, or both None (in place)")
-    caches_out, weights_out = (caches, weights) if in_place else (tuple(caches_out), weights_out)
+    if caches_out is None:
+        caches_out, weights_out = caches, weights
     if len(caches_out) != len(caches):
         raise ValueError("caches_out must hold one tensor for each of caches")
-    L_out = weights_out.shape[-1]
+    index, (B, Hkv, L), L_out = weights.get_device(), weights.shape, weights_out.shape[-1]
+    kept = torch.empty((B, Hkv, min(max(budget, 0), L)), dtype=_I32, device=index)
+    if seqlens_out is None:
+        seqlens_out = torch.empty((B,), dtype=_I32, device=index)
     n = len(caches)
-    with _Launch(weights, stream) as on:
-        kept = torch.empty((B, Hkv, min(max(budget, 0), L)), dtype=torch.int32, device=weights.device)
-        if seqlens_out is None:
-            seqlens_out = torch.empty((B,), dtype=torch.int32, device=weights.device)
-        src = [on.ptr(t, "caches", (B, Hkv, L, *t.shape[3:]), t.dtype) for t in caches]
-        dst = [on.ptr(o, "caches_out", (B, Hkv, L_out, *t.shape[3:]), t.dtype) for t, o in zip(caches, caches_out)]
-        row = [t.element_size() * math.prod(t.shape[3:]) for t in caches]
-        rc = lib.plx_cache_evict(n, (_vp * n)(*src), (_vp * n)(*dst), (_i * n)(*row),
-                                 on.ptr(weights, "weights", (B, Hkv, L), torch.float32),
-                                 on.ptr(weights_out, "weights_out", (B, Hkv, L_out), torch.float32),
-                                 on.ptr(seqlens, "seqlens", (B,), torch.int32),
-                                 on.ptr(seqlens_out, "seqlens_out", (B,), torch.int32),
-                                 kept.data_ptr(), B, Hkv, L, L_out, budget, sinks, recent, on.raw_stream())
+    src, dst, row = (_vp * n)(), (_vp * n)(), (_i * n)()
+    for i, (t, o) in enumerate(zip(caches, caches_out)):
+        rest = t.shape[3:]
+        src[i] = _ptr(t, "caches", (B, Hkv, L, *rest), t.dtype, index)
+        dst[i] = _ptr(o, "caches_out", (B, Hkv, L_out, *rest), t.dtype, index)
+        row[i] = t.element_size() * math.prod(rest)
+    rc = lib.plx_cache_evict(n, src, dst, row, _ptr(weights, "weights", (B, Hkv, L), _F32, index),
+                             _ptr(weights_out, "weights_out", (B, Hkv, L_out), _F32, index),
+                             _ptr(seqlens, "seqlens", (B,), _I32, index),
+                             _ptr(seqlens_out, "seqlens_out", (B,), _I32, index), kept.data_ptr(), B, Hkv, L, L_out,
+                             budget, sinks, recent, _raw_stream(index))
     _check(rc, "plx_cache_evict")
     return kept, seqlens_out
 
