@@ -26,7 +26,7 @@ LIBS = {
         "srcs": ["plx_api.cu", "simt.cu", "decode_mma.cu", "prefill_tc.cu", "norm_rope.cu",
                  "decode_noalloc.cu", "decode_gqa.cu", "decode_gqa_tc.cu", "backward_tc.cu", "fp8_linear.cu", "decode_fp8kv.cu",
                  "kv_int4.cu", "decode_cache.cu", "cache_evict.cu"],
-        "deps": ["plx_internal.cuh", "sm100.cuh", "decode_tc_common.cuh"],
+        "deps": ["plx_internal.cuh", "sm100.cuh", "decode_tc_common.cuh", "launch.cuh"],
         "link": ["-lcublas", "-lcublasLt", f"-Xlinker", f"-rpath={os.path.join(CUDA_HOME, 'lib64')}"],
     },
     "libplx_synth.so": {

@@ -46,6 +46,7 @@
 // What bounds it now: instructions.  15.5 a key and warp at G = 1, d = 128 (ALU
 // pipe 55 %, MMA pipe 31 %, issue slots 59 % busy with the 16 warps that registers
 // allow): 64 x 16 sequences of 4096 keys take 103 us, 5.5 TB/s, 0.85 of a copy's rate.
+#include "launch.cuh"
 #include "plx_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -112,8 +113,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -1095,30 +1094,6 @@ __global__ void __launch_bounds__(kFinThreads) cache_weights_kernel(const CacheD
   }
 }
 
-template <typename Kern, typename... Args>
-cudaError_t launch(Kern kern, unsigned grid, unsigned block, size_t smem, int cluster, cudaStream_t st,
-                   Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  // The kernel may be set up while the one before it in the stream drains; it
-  // waits for that one's end before it touches memory.
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.numAttrs = 1;
-  if (cluster > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-  }
-  cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <bool I4, int D, int G, bool W>
 cudaError_t run(const CacheDecodeArgs& a, cudaStream_t st) {
   const int smem = a.shares > 0 ? Tile<I4, D>::kRing : kSmem<I4, D, G>;
@@ -1133,17 +1108,17 @@ cudaError_t run(const CacheDecodeArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     set.fetch_or(1ull << a.device, std::memory_order_release);
   }
-  e = a.shares > 0 ? launch(kern, a.shares / kWarps, kThreads, smem, 1, st, a)
-                   : launch(kern, units * a.splits, kThreads, smem, a.splits, st, a);
+  e = a.shares > 0 ? launch_dependent(kern, a.shares / kWarps, kThreads, smem, 1, st, a)
+                   : launch_dependent(kern, units * a.splits, kThreads, smem, a.splits, st, a);
   if (e != cudaSuccess) return e;
   if constexpr (W) {
     const int parts = (a.L + kFinKeys - 1) / kFinKeys;
-    return launch(cache_weights_kernel<D, G>, units * parts, kFinThreads, 0, 1, st, a, parts);
+    return launch_dependent(cache_weights_kernel<D, G>, units * parts, kFinThreads, 0, 1, st, a, parts);
   } else {
     if (a.shares == 0) return cudaSuccess;
     // As many threads as there are records to read at once.
-    return a.shares <= 8 * units ? launch(cache_merge_kernel<D, G, 128>, units * G, 128, 0, 1, st, a)
-                                 : launch(cache_merge_kernel<D, G, 512>, units * G, 512, 0, 1, st, a);
+    return a.shares <= 8 * units ? launch_dependent(cache_merge_kernel<D, G, 128>, units * G, 128, 0, 1, st, a)
+                                 : launch_dependent(cache_merge_kernel<D, G, 512>, units * G, 512, 0, 1, st, a);
   }
 }
 

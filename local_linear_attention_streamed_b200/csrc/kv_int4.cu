@@ -28,6 +28,7 @@
 // Bound: HBM.  2 d bytes of bf16 and d/2 + 4 bytes of codes and word a row; a
 // division an element would cost more than the stream (84 us for 8 x 16 x 4096
 // rows of 128, where this takes 33).
+#include "launch.cuh"
 #include "plx_internal.cuh"
 
 #include <math_constants.h>
@@ -184,8 +185,8 @@ __global__ void __launch_bounds__(kThreads) kv_dequantize_int4_kernel(const uint
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv_append_int4_kernel(Int4AppendArgs a) {
   constexpr int N = kPieces<D>, kLanes = D / 8;
-  // The next kernel (a decode over this cache) may be set up meanwhile; it waits for this one's end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dep_wait();
+  grid_dep_launch();
   const int per = a.B * a.Hkv, t = threadIdx.x % kRowLanes;
   const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) / kRowLanes;  // K rows, then V rows
   const bool live = row < 2ll * per, isv = row >= per;
@@ -254,14 +255,9 @@ cudaError_t launch_kv_dequantize_int4(const void* codes, const void* params, voi
 cudaError_t launch_kv_append_int4(const Int4AppendArgs& a, cudaStream_t st) {
   const long long threads = 2ll * a.B * a.Hkv * kRowLanes;
   const unsigned grid = (unsigned)((threads + kThreads - 1) / kThreads);
-  if (a.d == 128) {
-    kv_append_int4_kernel<128><<<grid, kThreads, 0, st>>>(a);
-  } else if (a.d == 64) {
-    kv_append_int4_kernel<64><<<grid, kThreads, 0, st>>>(a);
-  } else {
-    return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  if (a.d != 64 && a.d != 128) return cudaErrorInvalidValue;
+  return launch_dependent(a.d == 128 ? kv_append_int4_kernel<128> : kv_append_int4_kernel<64>, grid, kThreads, 0, 1, st,
+                          a);
 }
 
 }  // namespace plx

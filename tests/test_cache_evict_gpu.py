@@ -143,6 +143,41 @@ def test_lengths_in_place_and_bad_lengths(plx):
     assert kept[0, 1].tolist() == ids.tolist()
 
 
+def test_lengths_in_place_with_many_caches(plx):
+    """New lengths are written while other CTAs still compact: nothing may depend on which comes first."""
+    B, Hkv, L, budget = 16, 8, 700, 100
+    w, caches = make(9, B, Hkv, L)
+    lens = [700 - 13 * b for b in range(B)]
+    for _ in range(5):
+        t, wd = [c.cuda() for c in caches], w.cuda()
+        sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        kept, new = plx.cache_evict(t, wd, sl, budget, 1, 8, seqlens_out=sl)
+        assert sl.tolist() == [budget] * B
+        at = kept.long()
+        for c, d in zip(caches, t):
+            idx = at.view(*at.shape, *([1] * (c.dim() - 3))).expand(*at.shape, *c.shape[3:])
+            assert np.array_equal(raw(d[:, :, :budget]), raw(torch.gather(c.cuda(), 2, idx)))
+            assert np.array_equal(raw(d[:, :, budget:]), raw(c[:, :, budget:]))
+        assert torch.equal(wd[..., :budget], torch.gather(w.cuda(), 2, at)) and not wd[..., budget:].any()
+
+
+@pytest.mark.parametrize("B,L", [(1, 5000), (2, 32768), (1, 40000), (160, 4200), (150, 17000), (150, 33000)])
+def test_every_select(plx, B, L):
+    """Clusters and single CTAs, totals in registers or read again, with many ties."""
+    g = torch.Generator(device="cuda").manual_seed(L)
+    w = torch.randint(0, 40, (B, 1, L), generator=g, device="cuda").float()
+    lens = torch.randint(L // 2, L + 1, (B,), generator=g, device="cuda").to(torch.int32)
+    lens[0] = L
+    budget, sinks, recent = L // 3, 4, 50
+    kept, new = plx.cache_evict([], w, lens, budget, sinks, recent, caches_out=[],
+                                weights_out=torch.empty((B, 1, budget), device="cuda"))
+    pos = torch.arange(L, device="cuda")
+    must = (pos < sinks) | ((pos >= lens[:, None, None] - recent) & (pos < lens[:, None, None]))
+    rank = torch.where(must, 1e9, torch.where(pos < lens[:, None, None], w, -1.0))
+    want = torch.sort(torch.sort(-rank, stable=True).indices[..., :budget]).values
+    assert torch.equal(kept.long(), want) and (new == budget).all()
+
+
 def test_graph_replays_with_new_lengths(plx):
     B, Hkv, L, budget = 2, 2, 200, 64
     w, caches = make(7, B, Hkv, L)
