@@ -433,29 +433,49 @@ struct Weights {
   uint32_t hi[Tile<I4, D>::kKeys / 16][(G + 3) / 4][2], lo[Tile<I4, D>::kKeys / 16][(G + 3) / 4][2];
 };
 
+// With G <= 2 and two blocks a tile, lanes t and t ^ G hold the same scores: the
+// one with bit G of t clear weighs block 0, the other block 1.
+template <bool I4, int D, int G>
+constexpr bool kHalves = G <= 2 && Tile<I4, D>::kKeys == 32;
+
 template <bool I4, int D, int G, bool W>
 __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4, D, G>& wt, const Scores<I4, D, G>& sco,
                                            uint32_t stage, const Query<D, (G + 3) / 4>& q,
                                            float* __restrict__ scores, int j0, int n, int lane) {
   using T = Tile<I4, D>;
   using Sc = Scores<I4, D, G>;
-  constexpr int NT = Sc::NT, NB = Sc::NB, KS = D / 16;
+  constexpr bool kHalf = kHalves<I4, D, G>;
+  constexpr int NT = Sc::NT, KS = D / 16, NB = kHalf ? 1 : Sc::NB;  // blocks this lane weighs
   const int g = lane >> 2, t = lane & 3;
+  const bool second = kHalf && (t & G);
+  const int key0 = g + (second ? 16 : 0);
   float sc[NB][NT][2], tt[NB][NT][2], sv[NB][2];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int key = 16 * b + g + 8 * r;
+      const int key = key0 + 16 * b + 8 * r;
       uint32_t pk = 0u, pv = 0u;
       if constexpr (I4) lds64(pk, pv, stage + T::kPOff + 8 * key);
       sv[b][r] = I4 ? bf_lo(pv) : 1.f;
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        float s1 = sco.S[b][u][0][2 * r], s2 = sco.S[b][u][0][2 * r + 1];
-        if constexpr (Sc::NC == 2) {
-          s1 += sco.S[b][u][1][2 * r];
-          s2 += sco.S[b][u][1][2 * r + 1];
+        float s1, s2;
+        if constexpr (kHalf) {
+          float x[2][2];
+#pragma unroll
+          for (int c = 0; c < Sc::NC; ++c) {
+            x[c][0] = second ? sco.S[1][u][c][2 * r] : sco.S[0][u][c][2 * r];
+            x[c][1] = second ? sco.S[1][u][c][2 * r + 1] : sco.S[0][u][c][2 * r + 1];
+          }
+          s1 = Sc::NC == 2 ? x[0][0] + x[1][0] : x[0][0];
+          s2 = Sc::NC == 2 ? x[0][1] + x[1][1] : x[0][1];
+        } else {
+          s1 = sco.S[b][u][0][2 * r], s2 = sco.S[b][u][0][2 * r + 1];
+          if constexpr (Sc::NC == 2) {
+            s1 += sco.S[b][u][1][2 * r];
+            s2 += sco.S[b][u][1][2 * r + 1];
+          }
         }
         if constexpr (I4) {  // sums of raw codes: the zero point times the row's sum goes off
           const float z = bf_hi(pk), sk = bf_lo(pk);
@@ -467,7 +487,8 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
         sc[b][u][r] = s1;
         tt[b][u][r] = s2;
         if constexpr (W) {
-          if (j0 + key < n && t < G) scores[(size_t)(j0 + key) * G + 4 * u + t] = s1;
+          const bool mine = kHalf ? t < 2 * G : t < G;
+          if (j0 + key < n && mine) scores[(size_t)(j0 + key) * G + 4 * u + (kHalf ? t & (G - 1) : t)] = s1;
         }
       }
     }
@@ -478,7 +499,7 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
       for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (j0 + 16 * b + g + 8 * r >= n) sc[b][u][r] = -CUDART_INF_F;
+          if (j0 + key0 + 16 * b + 8 * r >= n) sc[b][u][r] = -CUDART_INF_F;
   }
   bool raise = false;
 #pragma unroll
@@ -491,6 +512,7 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
       float mx = sc[0][u][0];
 #pragma unroll
       for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1]));
+      if constexpr (kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float m = mx > s.m[u] ? mx + kHeadroom : s.m[u];
@@ -517,10 +539,12 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
         const float p0 = I4 ? w * sv[b][r] : w, p1 = I4 ? w_t * sv[b][r] : w_t;
         const uint32_t h = pack_bf16(p0, p1);
         const uint32_t l = pack_bf16(p0 - bf_lo(h), p1 - bf_hi(h));
-        if constexpr (G == 1) {
-          wt.hi[b][u][r] = movmatrix_trans((t & 1) ? l : h);  // columns 4..7 repeat 0..3, unused
-        } else if constexpr (G == 2) {
-          wt.hi[b][u][r] = movmatrix_trans(t < 2 ? h : l);
+        if constexpr (kHalf) {  // hi in the columns with bit G of t clear, lo in the others
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, second ? h : l, G);
+          wt.hi[0][u][r] = movmatrix_trans(second ? other : h);
+          wt.hi[1][u][r] = movmatrix_trans(second ? l : other);
+        } else if constexpr (G <= 2) {
+          wt.hi[b][u][r] = movmatrix_trans((t & G) ? l : h);  // columns 4..7 repeat 0..3 for G = 1, unused
         } else {
           wt.hi[b][u][r] = movmatrix_trans(h);
           wt.lo[b][u][r] = movmatrix_trans(l);
@@ -602,6 +626,10 @@ __device__ __forceinline__ void write_records(State<D, (G + 3) / 4>& s, const Qu
   for (int u = 0; u < (G + 3) / 4; ++u) {
     const float f2 = I4 ? q.scale[u][1] : 1.f;  // of what holds t
     s.T[u] *= f2;
+    if constexpr (kHalves<I4, D, G>) {
+      s.omega[u] += __shfl_xor_sync(0xffffffffu, s.omega[u], G);
+      s.T[u] += __shfl_xor_sync(0xffffffffu, s.T[u], G);
+    }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       s.omega[u] += __shfl_xor_sync(0xffffffffu, s.omega[u], o);
