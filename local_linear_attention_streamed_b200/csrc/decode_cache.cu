@@ -986,86 +986,102 @@ struct Parts {
   __device__ __forceinline__ int slot(int c) const { return c == c0 ? unit : units + c; }
 };
 
-// Output of one head from its records, by all threads of a CTA: four dims a
-// lane, the records over groups of D / 4 lanes, each with its own running m.
-template <int D, int G, int kT>
-__device__ __forceinline__ void merge_output(const CacheDecodeArgs& a, const Parts& p, int h, float4 (*acc)[kT],
-                                             float4* head) {
-  constexpr int R = kRec<D>, kLanes = D / 4, kGroups = kT / kLanes;
-  const int dl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
-  float4 o1 = make_float4(0.f, 0.f, 0.f, 0.f), o2 = o1;
-  float m = kNoRef, omega = 0.f, tsum = 0.f;
-#pragma unroll 4
-  for (int c = p.c0 + grp; c <= p.c1; c += kGroups) {
-    const float4* rec = reinterpret_cast<const float4*>(a.records + ((size_t)p.slot(c) * G + h) * R);
-    const float4 x = rec[0], y1 = rec[1 + dl], y2 = rec[1 + kLanes + dl];
-    const float top = fmaxf(m, x.x), f0 = ex2(m - top), f = ex2(x.x - top);
-    m = top;
-    omega = f0 * omega + f * x.y;
-    tsum = f0 * tsum + f * x.z;
-    o1.x = f0 * o1.x + f * y1.x, o1.y = f0 * o1.y + f * y1.y, o1.z = f0 * o1.z + f * y1.z, o1.w = f0 * o1.w + f * y1.w;
-    o2.x = f0 * o2.x + f * y2.x, o2.y = f0 * o2.y + f * y2.y, o2.z = f0 * o2.z + f * y2.z, o2.w = f0 * o2.w + f * y2.w;
-  }
-  acc[0][threadIdx.x] = o1;
-  acc[1][threadIdx.x] = o2;
-  if (dl == 0) head[grp] = make_float4(m, omega, tsum, 0.f);
-  __syncthreads();
-  if (threadIdx.x < D) {
-    m = kNoRef;
-#pragma unroll
-    for (int c = 0; c < kGroups; ++c) m = fmaxf(m, head[c].x);
-    const float* f1 = reinterpret_cast<const float*>(acc[0]) + threadIdx.x;
-    const float* f2 = reinterpret_cast<const float*>(acc[1]) + threadIdx.x;
-    float x = 0.f, y = 0.f;
-    omega = tsum = 0.f;
-#pragma unroll
-    for (int c = 0; c < kGroups; ++c) {
-      const float f = ex2(head[c].x - m);
-      omega += f * head[c].y;
-      tsum += f * head[c].z;
-      x += f * f1[c * D];
-      y += f * f2[c * D];
-    }
-    const float inv = 1.f / omega;
-    static_cast<__nv_bfloat16*>(a.out)[((size_t)p.unit * G + h) * D + threadIdx.x] =
-        __float2bfloat16(((1.f + tsum * inv) * x - y) * inv);
-  }
-}
+// Outputs of HP heads from their records, by all kT threads of a CTA: four dims a
+// lane, a head's records over groups of D / 4 lanes, each with its own running m.
+template <int D, int G, int kT, int HP>
+struct Merge {
+  static constexpr int kLanes = D / 4, kGroups = kT / (HP * kLanes);
+  float4 o1[kT], o2[kT], head[HP * kGroups];
 
-// After a decode in shares: CTA (unit, h) merges head h of (b, KV head) `unit`.
-template <int D, int G, int kT>
+  __device__ __forceinline__ void run(const CacheDecodeArgs& a, const Parts& p, int h0) {
+    constexpr int R = kRec<D>;
+    const int dl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes % kGroups, hp = threadIdx.x / (kLanes * kGroups);
+    float4 x1 = make_float4(0.f, 0.f, 0.f, 0.f), x2 = x1;
+    float m = kNoRef, omega = 0.f, tsum = 0.f;
+#pragma unroll 4
+    for (int c = p.c0 + grp; c <= p.c1; c += kGroups) {
+      const float4* rec = reinterpret_cast<const float4*>(a.records + ((size_t)p.slot(c) * G + h0 + hp) * R);
+      const float4 x = rec[0], y1 = rec[1 + dl], y2 = rec[1 + kLanes + dl];
+      const float top = fmaxf(m, x.x), f0 = ex2(m - top), f = ex2(x.x - top);
+      m = top;
+      omega = f0 * omega + f * x.y;
+      tsum = f0 * tsum + f * x.z;
+      x1.x = f0 * x1.x + f * y1.x, x1.y = f0 * x1.y + f * y1.y;
+      x1.z = f0 * x1.z + f * y1.z, x1.w = f0 * x1.w + f * y1.w;
+      x2.x = f0 * x2.x + f * y2.x, x2.y = f0 * x2.y + f * y2.y;
+      x2.z = f0 * x2.z + f * y2.z, x2.w = f0 * x2.w + f * y2.w;
+    }
+    o1[threadIdx.x] = x1;
+    o2[threadIdx.x] = x2;
+    if (dl == 0) head[hp * kGroups + grp] = make_float4(m, omega, tsum, 0.f);
+    __syncthreads();
+    for (int e = threadIdx.x; e < HP * D; e += kT) {
+      const int i = e / D, dim = e % D;
+      m = kNoRef;
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) m = fmaxf(m, head[i * kGroups + c].x);
+      const float* f1 = reinterpret_cast<const float*>(o1) + i * kGroups * D + dim;
+      const float* f2 = reinterpret_cast<const float*>(o2) + i * kGroups * D + dim;
+      float x = 0.f, y = 0.f;
+      omega = tsum = 0.f;
+#pragma unroll
+      for (int c = 0; c < kGroups; ++c) {
+        const float4 r = head[i * kGroups + c];
+        const float f = ex2(r.x - m);
+        omega += f * r.y;
+        tsum += f * r.z;
+        x += f * f1[c * D];
+        y += f * f2[c * D];
+      }
+      const float inv = 1.f / omega;
+      static_cast<__nv_bfloat16*>(a.out)[((size_t)p.unit * G + h0 + i) * D + dim] =
+          __float2bfloat16(((1.f + tsum * inv) * x - y) * inv);
+    }
+  }
+};
+
+// After a decode in shares: HP heads of a (b, KV head) a CTA.
+template <int D, int G, int kT, int HP>
 __global__ void __launch_bounds__(kT) cache_merge_kernel(const CacheDecodeArgs a) {
-  __shared__ float4 acc[2][kT], head[kT / (D / 4)];
+  __shared__ Merge<D, G, kT, HP> merge;
   grid_dep_wait();
   grid_dep_launch();
-  const Parts p(a, blockIdx.x / G);
-  if (p.c0 >= 0) merge_output<D, G, kT>(a, p, blockIdx.x % G, acc, head);
+  const Parts p(a, blockIdx.x / (G / HP));
+  if (p.c0 >= 0) merge.run(a, p, blockIdx.x % (G / HP) * HP);
 }
 
 constexpr int kFinThreads = 256;
-constexpr int kFinKeys = 1024;  // keys of a CTA of the weights' kernel
+constexpr int kFinKeys = 2048;  // keys of a CTA that makes weights
 
-// Scores to weights: w_out = w_in + sum_h 2^(s_h - m_h) / omega_h.  After a
-// decode in shares it also merges the outputs: CTA `part` of the `parts` of a
-// (b, KV head) the heads part, part + parts, ...
+// Scores to weights: w_out = w_in + sum_h 2^(s_h - m_h) / omega_h, kFinKeys keys of
+// a (b, KV head) a CTA.  After a decode in shares the first CTAs merge outputs
+// instead, kFinHeads heads each.
+template <int D, int G>
+constexpr int kFinHeads = G < 128 / (D / 4) ? G : 128 / (D / 4);  // two groups of records a head at least
 template <int D, int G>
 __global__ void __launch_bounds__(kFinThreads) cache_weights_kernel(const CacheDecodeArgs a, int parts) {
-  constexpr int kTurns = kFinKeys / kFinThreads;
+  constexpr int kTurns = kFinKeys / kFinThreads, HP = kFinHeads<D, G>;
   __shared__ float sm[G], sinv[G];
-  __shared__ float4 acc[2][kFinThreads], head[kFinThreads / (D / 4)];
-  const int unit = blockIdx.x / parts, part = blockIdx.x % parts;
+  __shared__ Merge<D, G, kFinThreads, HP> merge;
+  int id = blockIdx.x;
+  const int merging = a.shares > 0 ? a.B * a.H / HP : 0;
   grid_dep_wait();
   grid_dep_launch();
-  const int n = a.seqlens[unit / a.Hkv];
-  if (bad_len(n, a.L) || (part * kFinKeys >= n && part >= G)) return;
-  // Scores and totals do not wait for the statistics.
+  if (id < merging) {
+    const Parts p(a, id / (G / HP));
+    if (p.c0 >= 0) merge.run(a, p, id % (G / HP) * HP);
+    return;
+  }
+  id -= merging;
+  const int unit = id / parts, part = id % parts;
+  // Scores and totals do not wait for the length and the statistics: what lies
+  // behind the length is read (inside of the arrays) and not used.
   const size_t row0 = (size_t)unit * a.L + part * kFinKeys;
-  const int here = n - part * kFinKeys;
+  const int room = a.L - part * kFinKeys;
   float x[kTurns][G], w[kTurns];
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
-    const int j = i * kFinThreads + threadIdx.x;
-    if (j >= here) continue;
+    const int j = min(i * kFinThreads + (int)threadIdx.x, room - 1);
     const float* sc = a.scores + (row0 + j) * G;
     if constexpr (G >= 4) {
 #pragma unroll
@@ -1077,14 +1093,16 @@ __global__ void __launch_bounds__(kFinThreads) cache_weights_kernel(const CacheD
     }
     w[i] = a.w_in[row0 + j];
   }
+  const int n = a.seqlens[unit / a.Hkv];
   const int lane = threadIdx.x & 31;
   if (a.shares > 0) {
     const Parts p(a, unit);
+    if (p.c0 < 0) return;
     for (int h = threadIdx.x >> 5; h < G; h += kFinThreads / 32) {
       float m = kNoRef, omega = 0.f;
 #pragma unroll 4
       for (int c = p.c0 + lane; c <= p.c1; c += 32) {
-            const float2 r = *reinterpret_cast<const float2*>(a.records + ((size_t)p.slot(c) * G + h) * kRec<D>);
+        const float2 r = *reinterpret_cast<const float2*>(a.records + ((size_t)p.slot(c) * G + h) * kRec<D>);
         const float top = fmaxf(m, r.x);
         omega = omega * ex2(m - top) + r.y * ex2(r.x - top);
         m = top;
@@ -1101,16 +1119,16 @@ __global__ void __launch_bounds__(kFinThreads) cache_weights_kernel(const CacheD
         sinv[h] = 1.f / omega;
       }
     }
-    for (int h = part; h < G; h += parts) {
-      merge_output<D, G, kFinThreads>(a, p, h, acc, head);
-      __syncthreads();
+  } else {
+    if (bad_len(n, a.L)) return;
+    if (threadIdx.x < G) {
+      const float2 r = a.stats[(size_t)unit * G + threadIdx.x];
+      sm[threadIdx.x] = r.x;
+      sinv[threadIdx.x] = 1.f / r.y;
     }
-  } else if (threadIdx.x < G) {
-    const float2 r = a.stats[(size_t)unit * G + threadIdx.x];
-    sm[threadIdx.x] = r.x;
-    sinv[threadIdx.x] = 1.f / r.y;
   }
   __syncthreads();
+  const int here = n - part * kFinKeys;
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
     const int j = i * kFinThreads + threadIdx.x;
@@ -1141,12 +1159,15 @@ cudaError_t run(const CacheDecodeArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if constexpr (W) {
     const int parts = (a.L + kFinKeys - 1) / kFinKeys;
-    return launch_dependent(cache_weights_kernel<D, G>, units * parts, kFinThreads, 0, 1, st, a, parts);
+    return launch_dependent(cache_weights_kernel<D, G>, units * parts + (a.shares > 0 ? units * G / kFinHeads<D, G> : 0),
+                            kFinThreads, 0, 1, st, a, parts);
   } else {
     if (a.shares == 0) return cudaSuccess;
-    // As many threads as there are records to read at once.
-    return a.shares <= 8 * units ? launch_dependent(cache_merge_kernel<D, G, 128>, units * G, 128, 0, 1, st, a)
-                                 : launch_dependent(cache_merge_kernel<D, G, 512>, units * G, 512, 0, 1, st, a);
+    // Few records each: up to four heads a CTA, four groups a head.  Many: a CTA a head.
+    constexpr int HP = G < 4 ? G : 4;
+    return a.shares <= 8 * (long long)units
+               ? launch_dependent(cache_merge_kernel<D, G, HP * D, HP>, units * (G / HP), HP * D, 0, 1, st, a)
+               : launch_dependent(cache_merge_kernel<D, G, 512, 1>, units * G, 512, 0, 1, st, a);
   }
 }
 
