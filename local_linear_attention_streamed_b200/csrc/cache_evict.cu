@@ -249,12 +249,13 @@ __global__ void __launch_bounds__(W * 32) evict_select_kernel(const EvictArgs a)
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 128;  // kept rows of a CTA
-constexpr int kMoveUnroll = 4;
+constexpr int kMoveRows = 1024;  // kept rows of a CTA, at most
+constexpr int kMoveUnroll = 8;
 
 struct MoveList {
   int vec[kEvictMaxCaches + 1];    // bytes a thread moves at once: 16, 4 or 1
   int shift[kEvictMaxCaches + 1];  // log2 of the pieces of a row; -1: no power of two
+  int rows;                        // kept rows of a CTA
 };
 
 template <typename V, bool kShift>
@@ -328,10 +329,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
       }
     }
   } else {
-    const int i0 = part * kMoveRows, rows = min(nk - i0, kMoveRows);
+    const int i0 = part * list.rows, rows = min(nk - i0, list.rows);
     if (rows > 0) {
       __shared__ int ids[kMoveRows];
-      if (threadIdx.x < rows) ids[threadIdx.x] = kept[i0 + threadIdx.x];
+      for (int i = threadIdx.x; i < rows; i += kMoveThreads) ids[i] = kept[i0 + i];
       __syncthreads();
       dst += (size_t)i0 * rb;
       auto run = [&](auto piece) {
@@ -397,7 +398,11 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st, int num_sms)
       if (pieces == 1 << k) list.shift[c] = k;
   }
   const int room = a.budget < a.L ? a.budget : a.L;
-  const int parts = (room + kMoveRows - 1) / kMoveRows;
+  // Long runs of rows where they still make four CTAs an SM (64 x 8 batch of 1024
+  // rows of 256 bytes: 97 us, with runs of 256 104 us, of 128 109 us).
+  const long long runs = (long long)units * ((room + kMoveRows - 1) / kMoveRows) * a.count;
+  list.rows = runs >= 4ll * num_sms ? kMoveRows : kMoveRows / 4;
+  const int parts = (room + list.rows - 1) / list.rows;
   return launch_dependent(evict_move_kernel, dim3(units * parts, a.count + 1), kMoveThreads, 0, 1, st, a, list, parts);
 }
 
