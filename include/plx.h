@@ -394,7 +394,9 @@ int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams
  * [B, Hkv, L, 2]; seqlens int32 [B] in 1..L (others write zeros and report
  * PLX_ERR_BAD_SEQLEN).  Query head h reads KV head h / (H/Hkv), groups of 1, 2, 4
  * or 8; d in {64, 128}, else PLX_ERR_UNSUPPORTED.  Cache rows at and behind
- * seqlens[b] are not read.  It reads 2 (d/2 + 4) bytes a cached key.
+ * seqlens[b] are not read.  It reads 2 (d/2 + 4) bytes a cached key.  Elements of
+ * q and r up to 2^120 in magnitude are computed with; larger ones give infinities
+ * or NaN.
  * workspace: plx_decode_int4kv_workspace_bytes() bytes, 256-byte aligned, no
  * initial contents; NULL is allowed where that is 0, else PLX_ERR_WORKSPACE.
  * Nothing else is shared between calls: calls with different workspaces may run

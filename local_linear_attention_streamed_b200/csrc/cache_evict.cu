@@ -17,8 +17,8 @@
 // * move: CTAs over (b, KV head), kept rows and caches; the totals are one more
 //   cache of 4-byte rows, with zeros behind the last.  A row moved within its
 //   cache goes to a lower index, so an in-place cache is compacted by one CTA a
-//   (b, KV head) that reads a run of rows, waits, and writes it: rows still to
-//   be read always lie behind those written.
+//   (b, KV head) and slice of the rows that reads a run, waits, and writes it:
+//   rows still to be read always lie behind those written.
 #include "launch.cuh"
 #include "plx_internal.cuh"
 
@@ -256,6 +256,7 @@ struct MoveList {
   int vec[kEvictMaxCaches + 1];    // bytes a thread moves at once: 16, 4 or 1
   int shift[kEvictMaxCaches + 1];  // log2 of the pieces of a row; -1: no power of two
   int rows;                        // kept rows of a CTA
+  int slices;                      // of an in-place cache's rows, at most
 };
 
 template <typename V, bool kShift>
@@ -279,22 +280,32 @@ __device__ __forceinline__ void move_rows(const V* src, V* dst, const int* kept,
   }
 }
 
-// Within one cache: a run is read by all threads before any of it is written.
+// Within one cache, pieces [first, first + width) of its rows: a run is read by all
+// threads before any of it is written.
+constexpr int kCompactUnroll = 16;
 template <typename V>
-__device__ __forceinline__ void compact_rows(V* rows, const int* kept, int nk, int per_row) {
-  const long long total = (long long)nk * per_row;
-  for (long long base = 0; base < total; base += kMoveUnroll * kMoveThreads) {
-    V v[kMoveUnroll];
+__device__ __forceinline__ void compact_rows(V* rows, const int* kept, int nk, int per_row, int first, int width) {
+  const int shift = (width & (width - 1)) == 0 ? __ffs(width) - 1 : -1;
+  const long long total = (long long)nk * width;
+  rows += first;
+  for (long long base = 0; base < total; base += kCompactUnroll * kMoveThreads) {
+    V v[kCompactUnroll];
 #pragma unroll
-    for (int e = 0; e < kMoveUnroll; ++e) {
+    for (int e = 0; e < kCompactUnroll; ++e) {
       const long long x = base + e * kMoveThreads + threadIdx.x;
-      if (x < total) v[e] = rows[(long long)kept[x / per_row] * per_row + x % per_row];
+      if (x < total) {
+        const long long row = shift >= 0 ? x >> shift : x / width;
+        v[e] = rows[(long long)kept[row] * per_row + (x - row * width)];
+      }
     }
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < kMoveUnroll; ++e) {
+    for (int e = 0; e < kCompactUnroll; ++e) {
       const long long x = base + e * kMoveThreads + threadIdx.x;
-      if (x < total) rows[x] = v[e];
+      if (x < total) {
+        const long long row = shift >= 0 ? x >> shift : x / width;
+        rows[row * per_row + (x - row * width)] = v[e];
+      }
     }
     __syncthreads();
   }
@@ -318,14 +329,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   char* dst = static_cast<char*>(totals ? static_cast<void*>(a.w_out) : a.dst[c]) + (size_t)unit * a.Lout * rb;
   const int vec = list.vec[c];
   if (src == dst) {
-    if (part != 0) return;
-    if (nk > 0 && kept[nk - 1] != nk - 1) {  // else every row is in its place
+    // Slices of a row, 64 bytes or more, move on their own.
+    const int slices = max(1, min(min(parts, list.slices), rb / 64));
+    const bool mine = part < slices && nk > 0 && kept[nk - 1] != nk - 1;  // else every row is in its place
+    if (mine) {
+      auto run = [&](auto piece) {
+        using V = decltype(piece);
+        const int pieces = rb / (int)sizeof(V), each = (pieces + slices - 1) / slices;
+        const int first = part * each, width = min(each, pieces - first);
+        if (width > 0) compact_rows(reinterpret_cast<V*>(dst), kept, nk, pieces, first, width);
+      };
       if (vec == 16) {
-        compact_rows(reinterpret_cast<uint4*>(dst), kept, nk, rb / 16);
+        run(uint4());
       } else if (vec == 4) {
-        compact_rows(reinterpret_cast<uint32_t*>(dst), kept, nk, rb / 4);
+        run(uint32_t());
       } else {
-        compact_rows(reinterpret_cast<uint8_t*>(dst), kept, nk, rb);
+        run(uint8_t());
       }
     }
   } else {
@@ -403,6 +422,9 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st, int num_sms)
   const long long runs = (long long)units * ((room + kMoveRows - 1) / kMoveRows) * a.count;
   list.rows = runs >= 4ll * num_sms ? kMoveRows : kMoveRows / 4;
   const int parts = (room + list.rows - 1) / list.rows;
+  // In place, slices only where whole rows leave SMs idle (8 x 131072 rows to half:
+  // 0.83 ms, whole 2.25 ms; 64 x 8 x 4096 to a quarter: 0.21 ms, whole 0.16 ms).
+  list.slices = (long long)units * a.count >= 2ll * num_sms ? 1 : parts;
   return launch_dependent(evict_move_kernel, dim3(units * parts, a.count + 1), kMoveThreads, 0, 1, st, a, list, parts);
 }
 

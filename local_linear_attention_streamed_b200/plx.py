@@ -653,6 +653,8 @@ def cache_evict(caches, weights, seqlens, budget: int, sinks: int = 0, recent: i
         caches_out, weights_out = caches, weights
     if len(caches_out) != len(caches):
         raise ValueError("caches_out must hold one tensor for each of caches")
+    if max(budget, sinks, recent) >= 1 << 31:
+        raise ValueError("budget, sinks and recent must be below 2^31")
     index, (B, Hkv, L), L_out = weights.get_device(), weights.shape, weights_out.shape[-1]
     kept = torch.empty((B, Hkv, min(max(budget, 0), L)), dtype=_I32, device=index)
     if seqlens_out is None:
