@@ -282,7 +282,7 @@ __device__ __forceinline__ void move_rows(const V* src, V* dst, const int* kept,
 
 // Within one cache, pieces [first, first + width) of its rows: a run is read by all
 // threads before any of it is written.
-constexpr int kCompactUnroll = 16;
+constexpr int kCompactUnroll = 8;
 template <typename V>
 __device__ __forceinline__ void compact_rows(V* rows, const int* kept, int nk, int per_row, int first, int width) {
   const int shift = (width & (width - 1)) == 0 ? __ffs(width) - 1 : -1;
@@ -423,7 +423,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st, int num_sms)
   list.rows = runs >= 4ll * num_sms ? kMoveRows : kMoveRows / 4;
   const int parts = (room + list.rows - 1) / list.rows;
   // In place, slices only where whole rows leave SMs idle (8 x 131072 rows to half:
-  // 0.83 ms, whole 2.25 ms; 64 x 8 x 4096 to a quarter: 0.21 ms, whole 0.16 ms).
+  // 0.89 ms, whole 2.25 ms; a batch of 64 x 8 x 4096 to a quarter, whole: 0.16 ms).
   list.slices = (long long)units * a.count >= 2ll * num_sms ? 1 : parts;
   return launch_dependent(evict_move_kernel, dim3(units * parts, a.count + 1), kMoveThreads, 0, 1, st, a, list, parts);
 }
