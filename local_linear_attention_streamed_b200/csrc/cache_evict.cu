@@ -269,7 +269,7 @@ __device__ __forceinline__ void move_rows(const V* src, V* dst, const int* kept,
       const int x = base + e * kMoveThreads;
       if (x < total) {
         const int row = kShift ? x >> shift : x / per_row;
-        v[e] = src[(size_t)kept[row] * per_row + (x - row * per_row)];
+        v[e] = __ldcs(src + (size_t)kept[row] * per_row + (x - row * per_row));  // read once
       }
     }
 #pragma unroll
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
       } else if (vec == 4) {
         run(uint32_t());
       } else {
-        run(uint8_t());
+        run((unsigned char)0);
       }
     }
   } else {
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
       } else if (vec == 4) {
         run(uint32_t());
       } else {
-        run(uint8_t());
+        run((unsigned char)0);
       }
       dst -= (size_t)i0 * rb;
     }

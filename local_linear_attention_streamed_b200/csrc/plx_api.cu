@@ -728,6 +728,7 @@ static int cache_decode_impl(const void* q, const void* r, const void* K, const 
   a.d = d;
   a.splits = need.splits;
   a.shares = need.shares;
+  a.once = need.once;
   if (need.shares > 0) {
     a.records = reinterpret_cast<float*>(ws + need.records);
     a.parts = reinterpret_cast<int2*>(ws + need.parts);
