@@ -43,9 +43,11 @@
 // workspace that a second kernel merges.  There are no counters and no
 // library-owned memory: calls on several streams are independent.
 //
-// What bounds it now: instructions.  15.5 a key and warp at G = 1, d = 128 (ALU
-// pipe 55 %, MMA pipe 31 %, issue slots 59 % busy with the 16 warps that registers
-// allow): 64 x 16 sequences of 4096 keys take 103 us, 5.5 TB/s, 0.85 of a copy's rate.
+// What bounds it now: instructions.  15.0 a key and warp at G = 1, d = 128, 17.5 at
+// G = 4 (issue slots 61 % and 55 % busy, the ALU pipe 61 % and 47 %, the MMA pipe
+// 33 % and 37 %, with the 16 warps an SM that registers allow; more warps with
+// smaller tiles were slower).  64 x 16 sequences of 4096 keys: 97 us, 5.9 TB/s, 0.9
+// of a copy's rate, on a rested GPU; 108 us at the clock that a long run keeps.
 #include "launch.cuh"
 #include "plx_internal.cuh"
 
