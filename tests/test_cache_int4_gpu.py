@@ -173,7 +173,8 @@ def test_decode_lengths(plx, G, Hkv, d):
 
 @pytest.mark.parametrize("B,Hkv,G,L,d", [
     (1, 1, 1, 5000, 128), (1, 2, 4, 9001, 64), (2, 1, 8, 4099, 128), (1, 1, 2, 40000, 64), (40, 3, 1, 700, 128),
-    (300, 4, 1, 40, 64), (7, 8, 2, 129, 128),
+    (300, 4, 1, 40, 64), (7, 8, 2, 129, 128), (200, 2, 1, 1100, 64), (1, 1, 8, 150000, 64), (1, 1, 1, 5, 128),
+    (225, 4, 4, 70, 128), (20, 4, 8, 900, 128),
 ])
 def test_decode_splits(plx, B, Hkv, G, L, d):
     """Every way a sequence is cut: many CTAs merged through the workspace, clusters, one CTA; repeatable."""
@@ -318,6 +319,34 @@ def test_bad_lengths_are_reported(plx):
         Vc, Vp, V = quantised(plx, c["V"])
 
 
+@pytest.mark.parametrize("B,Hkv,L", [(200, 2, 1100), (300, 3, 50)])
+def test_bad_lengths_in_a_large_batch(plx, B, Hkv, L):
+    """Every kind of launch skips the bad sequences and serves the others (first, last and neighbours among the bad)."""
+    d, G = 64, 1
+    c = case(8, B, Hkv, G, L, d)
+    Kc, Kp, K = quantised(plx, c["K"])
+    Vc, Vp, V = quantised(plx, c["V"])
+    q, r, w = c["q"].cuda(), c["r"].cuda(), c["w"].cuda()
+    g = torch.Generator().manual_seed(5)
+    sl = torch.randint(1, L + 1, (B,), generator=g, dtype=torch.int32)
+    bad = [0, 1, 63, 127, 128, 129, B - 1]
+    for i, b in enumerate(bad):
+        sl[b] = (0, L + 1, -1)[i % 3]
+    good = [b for b in range(B) if b not in bad]
+    wo = w.clone()
+    outs = [plx.decode_int4kv(q, r, Kc, Kp, Vc, Vp, sl.cuda(), out=torch.ones_like(q)),
+            plx.decode_int4kv_weights(q, r, Kc, Kp, Vc, Vp, sl.cuda(), wo, out=torch.ones_like(q))]
+    assert plx.get_device_status() == -6
+    for out in outs:
+        assert not out[bad].any()
+        check_out(out[good], f64(q)[good], f64(r)[good], K[good], V[good], sl[good].tolist())
+    assert torch.equal(wo[bad], w[bad])
+    check_weights(wo[good], f64(q)[good], f64(r)[good], K[good], V[good], sl[good].tolist(), w[good], w[good])
+    none = torch.zeros((B,), dtype=torch.int32, device="cuda")
+    out = plx.decode_int4kv_weights(q, r, Kc, Kp, Vc, Vp, none, wo)
+    assert plx.get_device_status() == -6 and not out.any()
+
+
 def test_binding_refuses(plx):
     B, Hkv, G, L, d = 2, 2, 2, 24, 64
     c = case(7, B, Hkv, G, L, d)
@@ -346,6 +375,11 @@ def test_binding_refuses(plx):
     flat = torch.zeros(w.numel() + 8, device="cuda")
     with pytest.raises(plx.PlxError):  # weights and weights_out overlap
         plx.decode_weights(q, r, K16, V16, sl, flat[:-8].view_as(w), weights_out=flat[8:].view_as(w))
+    shifted = torch.zeros(q.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view_as(q)
+    with pytest.raises(plx.PlxError):  # not 16-byte aligned
+        plx.decode_int4kv(shifted, *ok[1:])
+    with pytest.raises(plx.PlxError):  # workspace not 256-byte aligned
+        plx.decode_weights(q, r, K16, V16, sl, w, workspace=torch.empty(1 << 22, dtype=torch.uint8, device="cuda")[8:])
     with pytest.raises(plx.PlxError):  # group of three
         plx.decode_int4kv(torch.cat((q, q[:, :2]), 1), torch.cat((r, r[:, :2]), 1), *ok[2:])
     with pytest.raises(ValueError):
@@ -428,6 +462,47 @@ def test_two_graphs_and_eager_calls_between(plx):
             check_out(out, f64(q), f64(r), K, V, sl.tolist())
             check_out(out2, f64(q), f64(r), K, V, sl.tolist())
             check_weights(wo, f64(q), f64(r), K, V, sl.tolist(), w, torch.zeros_like(w))
+
+
+def test_two_graphs_at_once(plx):
+    """Captured calls of two sizes, replayed on two streams at the same time, with other calls on a third."""
+    runs = []
+    for i, (B, Hkv, G, L, d) in enumerate([(1, 2, 2, 9000, 128), (3, 2, 1, 4000, 64)]):
+        c = case(60 + i, B, Hkv, G, L, d)
+        Kc, Kp, _ = quantised(plx, c["K"])
+        Vc, Vp, _ = quantised(plx, c["V"])
+        sl = torch.full((B,), L - 5, dtype=torch.int32, device="cuda")
+        args = (c["q"].cuda(), c["r"].cuda(), Kc, Kp, Vc, Vp, sl)
+        w = c["w"].cuda()
+        want_w = w.clone()
+        want = plx.decode_int4kv_weights(*args, want_w)
+        wo, kept = torch.zeros_like(w), None
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = plx.decode_int4kv_weights(*args, w, weights_out=wo)
+            small = [torch.zeros((B, Hkv, 500, *t.shape[3:]), dtype=t.dtype, device="cuda") for t in (Kc, Kp)]
+            kept, _ = plx.cache_evict([Kc, Kp], wo, sl, 500, 2, 16, caches_out=small,
+                                      weights_out=torch.empty((B, Hkv, 500), device="cuda"))
+        runs.append((graph, torch.cuda.Stream(), args, out, wo, want, want_w, kept, small, L))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        other = plx.decode_int4kv(*runs[0][2], stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(other, plx.decode_int4kv(*runs[0][2]))
+    for _, _, args, out, wo, want, want_w, kept, small, L in runs:
+        assert torch.equal(out, want)
+        n = L - 5
+        assert torch.equal(wo[..., :n], want_w[..., :n])
+        at = kept.long()[..., None]
+        assert torch.equal(small[0], torch.gather(args[2], 2, at.expand(*at.shape[:3], args[2].shape[-1])))
+        for b in range(kept.shape[0]):
+            for h in range(kept.shape[1]):
+                assert kept[b, h].tolist() == oracle.evict_ref(want_w[b, h].tolist(), n, 500, 2, 16).tolist()
 
 
 @pytest.mark.parametrize("int4", [False, True])
