@@ -11,6 +11,8 @@ _BINDING_NAMES = {
     "get_device_status", "status_string", "PlxError", "lib", "PLX_F32", "PLX_BF16",
     "prefill_train", "prefill_backward", "prefill_bwd_workspace_bytes", "parallax_attention",
     "ParallaxAttention", "prefill_window", "decode_window", "layer_forward_fp8", "prefill_block_sparse", "prefill_gqa",
+    "kv_quantize_int4", "kv_dequantize_int4", "kv_append_int4", "decode_int4kv", "decode_int4kv_workspace_bytes",
+    "decode_weights", "decode_int4kv_weights", "decode_weights_workspace_bytes", "cache_evict",
 }
 
 
