@@ -8,6 +8,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -481,6 +482,12 @@ def _workspace(given, need: int, index: int):
     return given, given.data_ptr(), given.numel() * given.element_size()
 
 
+@functools.lru_cache(maxsize=256)
+def _bytes_needed(query: str, index: int, *sizes) -> int:
+    """Workspace of a call of these sizes on device ``index`` (the current one), by the entry point that tells it."""
+    return getattr(lib, query)(*sizes)
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device, as its address
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
@@ -564,7 +571,8 @@ def decode_int4kv(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, out=None, wor
     _, Hkv, L, _ = Kcodes.shape
     if out is None:
         out = torch.empty_like(q)
-    ws, ws_ptr, ws_bytes = _workspace(workspace, lib.plx_decode_int4kv_workspace_bytes(B, H, Hkv, L, d), index)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, _bytes_needed("plx_decode_int4kv_workspace_bytes", index, B, H, Hkv, L, d), index)
     rc = lib.plx_decode_int4kv(_ptr(q, "q", heads, _BF16, index), _ptr(r, "r", heads, _BF16, index),
                                *_int4_cache(Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d, index),
                                _ptr(seqlens, "seqlens", (B,), _I32, index), _ptr(out, "out", heads, _BF16, index),
@@ -592,7 +600,8 @@ def decode_weights(q, r, Kcache, Vcache, seqlens, weights, weights_out=None, out
         out = torch.empty_like(q)
     if weights_out is None:
         weights_out = weights
-    ws, ws_ptr, ws_bytes = _workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d), index)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, _bytes_needed("plx_decode_weights_workspace_bytes", index, B, H, Hkv, L, d), index)
     rc = lib.plx_decode_weights(_ptr(q, "q", heads, _BF16, index), _ptr(r, "r", heads, _BF16, index),
                                 _ptr(Kcache, "Kcache", cache, _BF16, index),
                                 _ptr(Vcache, "Vcache", cache, _BF16, index),
@@ -621,7 +630,8 @@ def decode_int4kv_weights(q, r, Kcodes, Kparams, Vcodes, Vparams, seqlens, weigh
         out = torch.empty_like(q)
     if weights_out is None:
         weights_out = weights
-    ws, ws_ptr, ws_bytes = _workspace(workspace, lib.plx_decode_weights_workspace_bytes(B, H, Hkv, L, d), index)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, _bytes_needed("plx_decode_weights_workspace_bytes", index, B, H, Hkv, L, d), index)
     rc = lib.plx_decode_int4kv_weights(_ptr(q, "q", heads, _BF16, index), _ptr(r, "r", heads, _BF16, index),
                                        *_int4_cache(Kcodes, Kparams, Vcodes, Vparams, B, Hkv, L, d, index),
                                        _ptr(seqlens, "seqlens", (B,), _I32, index),
