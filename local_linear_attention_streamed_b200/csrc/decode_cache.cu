@@ -1192,12 +1192,14 @@ cudaError_t pick(const CacheDecodeArgs& a, cudaStream_t st) {
 
 // How the keys are cut, by sizes alone.  Measured on a B200 with 4-bit rows, d =
 // 128, us with shares / one CTA a (b, KV head) / the best cluster of 2 to 8:
-//   many (b, KV head) balance themselves:  64 x 16 of 4096 keys     113 / 107 / 113
-//   fewer, or ragged, need shares:         64 x 8 of 2048..4096      57 /  64 /  64
-//                                          1 x 8 of 32768            27 / 182 /  33
-//   little work ends soonest in one launch: 8 x 8 of 2048..4096, G=4 23 /  29 /  18
-//                                          1 x 2 of 4096             12 /  30 /  12
-// (G = 4 but for the first; each includes about 8 us of an empty graph launch).
+//   many (b, KV head) balance themselves:   64 x 16 of 4096 keys           111 / 104 / 111
+//   (not where they are ragged:             64 x 16 of 2048..4096           86 /  92 /  92)
+//   fewer need shares:                      64 x 8 of 2048..4096, G = 4     57 /  64 /  68
+//                                           1 x 8 of 32768, G = 4           27 / 191 /  35
+//                                           1 x 2 of 32768                  18 / 188 /  35
+//   little work ends soonest in one launch: 8 x 8 of 2048..4096, G = 4      24 /  33 /  20
+//                                           1 x 2 of 4096, G = 4            12 /  30 /  12
+// (each includes about 8 us of an empty graph launch).
 // Weights take a second launch in any case, so only many units go without shares.
 CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool int4, bool weights) {
   CacheDecodeSpace w;
