@@ -453,7 +453,7 @@ constexpr bool kHalves = G <= 2 && Tile<I4, D>::kKeys == 32;
 template <bool I4, int D, int G, bool W>
 __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4, D, G>& wt, const Scores<I4, D, G>& sco,
                                            uint32_t stage, const Query<D, (G + 3) / 4>& q,
-                                           float* __restrict__ scores, int j0, int n, int lane) {
+                                           float* scores, int j0, int n, int lane) {
   using T = Tile<I4, D>;
   using Sc = Scores<I4, D, G>;
   constexpr bool kHalf = kHalves<I4, D, G>;

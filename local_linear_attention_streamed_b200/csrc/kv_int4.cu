@@ -134,12 +134,13 @@ __device__ __forceinline__ uint4 unpack_values(uint32_t c, uint32_t word) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_quantize_int4_kernel(const uint4* __restrict__ X,
-                                                                    uint32_t* __restrict__ codes,
-                                                                    uint32_t* __restrict__ params, long long rows) {
+__global__ void __launch_bounds__(kThreads) kv_quantize_int4_kernel(const uint4* X, uint32_t* codes, uint32_t* params,
+                                                                    long long rows) {
   constexpr int N = kPieces<D>, kRows = kThreads / kRowLanes;
   const int t = threadIdx.x % kRowLanes;
   const long long step = (long long)gridDim.x * kRows;
+  grid_dep_wait();  // (no __restrict__ here: loads that count as invariant may move above this)
+  grid_dep_launch();
   // Whole warps stay together for the shuffles.
   for (long long base = (long long)blockIdx.x * kRows + (threadIdx.x & ~31) / kRowLanes; base < rows; base += step) {
     const long long row = base + (threadIdx.x & 31) / kRowLanes, at = row * (D / 8) + t;
@@ -157,11 +158,12 @@ __global__ void __launch_bounds__(kThreads) kv_quantize_int4_kernel(const uint4*
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_dequantize_int4_kernel(const uint32_t* __restrict__ codes,
-                                                                      const uint32_t* __restrict__ params,
-                                                                      uint4* __restrict__ out, long long total) {
+__global__ void __launch_bounds__(kThreads) kv_dequantize_int4_kernel(const uint32_t* codes, const uint32_t* params,
+                                                                      uint4* out, long long total) {
   constexpr int kLanes = D / 8;
   const long long step = (long long)gridDim.x * kThreads * kUnroll;
+  grid_dep_wait();
+  grid_dep_launch();
   for (long long base = (long long)blockIdx.x * kThreads * kUnroll + threadIdx.x; base < total; base += step) {
     uint32_t c[kUnroll], w[kUnroll];
 #pragma unroll
@@ -222,34 +224,20 @@ cudaError_t launch_kv_quantize_int4(const void* X, void* codes, void* params, lo
                                     cudaStream_t st, int num_sms) {
   const long long blocks = (rows + kThreads / kRowLanes - 1) / (kThreads / kRowLanes);
   const unsigned grid = (unsigned)(blocks < 64ll * num_sms ? blocks : 64ll * num_sms);
-  auto x = static_cast<const uint4*>(X);
-  auto c = static_cast<uint32_t*>(codes);
-  auto p = static_cast<uint32_t*>(params);
-  if (d == 128) {
-    kv_quantize_int4_kernel<128><<<grid, kThreads, 0, st>>>(x, c, p, rows);
-  } else if (d == 64) {
-    kv_quantize_int4_kernel<64><<<grid, kThreads, 0, st>>>(x, c, p, rows);
-  } else {
-    return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  if (d != 64 && d != 128) return cudaErrorInvalidValue;
+  return launch_dependent(d == 128 ? kv_quantize_int4_kernel<128> : kv_quantize_int4_kernel<64>, grid, kThreads, 0, 1, st,
+                          static_cast<const uint4*>(X), static_cast<uint32_t*>(codes), static_cast<uint32_t*>(params),
+                          rows);
 }
 
 cudaError_t launch_kv_dequantize_int4(const void* codes, const void* params, void* out, long long rows, int d,
                                       cudaStream_t st, int num_sms) {
   const long long total = rows * (d / 8), blocks = (total + kThreads * kUnroll - 1) / (kThreads * kUnroll);
   const unsigned grid = (unsigned)(blocks < 64ll * num_sms ? blocks : 64ll * num_sms);
-  auto c = static_cast<const uint32_t*>(codes);
-  auto p = static_cast<const uint32_t*>(params);
-  auto o = static_cast<uint4*>(out);
-  if (d == 128) {
-    kv_dequantize_int4_kernel<128><<<grid, kThreads, 0, st>>>(c, p, o, total);
-  } else if (d == 64) {
-    kv_dequantize_int4_kernel<64><<<grid, kThreads, 0, st>>>(c, p, o, total);
-  } else {
-    return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+  if (d != 64 && d != 128) return cudaErrorInvalidValue;
+  return launch_dependent(d == 128 ? kv_dequantize_int4_kernel<128> : kv_dequantize_int4_kernel<64>, grid, kThreads, 0, 1,
+                          st, static_cast<const uint32_t*>(codes), static_cast<const uint32_t*>(params),
+                          static_cast<uint4*>(out), total);
 }
 
 cudaError_t launch_kv_append_int4(const Int4AppendArgs& a, cudaStream_t st) {

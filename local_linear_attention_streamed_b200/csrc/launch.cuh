@@ -6,7 +6,8 @@
 namespace plx {
 
 // Until the kernels before this one in the stream have ended and their writes
-// are visible; called before any access to memory that they may touch.
+// are visible; called before any access to memory that they may touch (through
+// pointers without __restrict__, whose loads might be moved above it).
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // From here on the next kernel in the stream may be set up, if it was launched
 // by launch_dependent (and calls grid_dep_wait).
