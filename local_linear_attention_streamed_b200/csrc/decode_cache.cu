@@ -29,6 +29,7 @@
 //   z (sum of q) goes off each score.  Value codes become (c - z) 2^-6 in one FMA
 //   first, exactly: sums over raw codes would be large, with small differences.
 //   The dims are paired as the nibbles fall; the other operand is permuted to match.
+//   Value codes come transposed, four keys of a byte in a register (ldmatrix on bytes).
 // * Groups of 1 and 2 leave columns free: the weights go in as bf16 hi + lo
 //   pairs there; larger groups issue a second MMA for the lo part.  So the
 //   weights keep 16 bits.
@@ -43,11 +44,11 @@
 // workspace that a second kernel merges.  There are no counters and no
 // library-owned memory: calls on several streams are independent.
 //
-// What bounds it now: instructions.  15.0 a key and warp at G = 1, d = 128, 17.5 at
-// G = 4 (issue slots 61 % and 55 % busy, the ALU pipe 61 % and 47 %, the MMA pipe
-// 33 % and 37 %, with the 16 warps an SM that registers allow; more warps with
-// smaller tiles were slower).  64 x 16 sequences of 4096 keys: 97 us, 5.9 TB/s, 0.9
-// of a copy's rate, on a rested GPU; 108 us at the clock that a long run keeps.
+// What bounds it now: instructions.  14.5 a key and warp at G = 1, d = 128, 17 at
+// G = 4 (issue slots 60 % and 55 % busy, the ALU pipe 58 % and 47 %, the MMA pipe
+// 34 % and 37 %; 12 or 20 warps an SM in place of 16 change nothing or lose).  64 x
+// 16 sequences of 4096 keys: 95 us, 6.0 TB/s, 0.92 of a copy's rate, on a rested
+// GPU; 105 to 112 us at the clock that a long run keeps.
 #include "launch.cuh"
 #include "plx_internal.cuh"
 
@@ -97,6 +98,15 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "r"(addr));
 }
 
+// Two 16 x 16 byte matrices, transposed: lane (g, t) gets bytes of rows 4t .. 4t + 3,
+// of column g and of column g + 8, for each.  Lanes 0-15 (16-31) give the first's
+// (second's) row addresses.
+__device__ __forceinline__ void ldmatrix2_bytes_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
 // 16- and 4-byte asynchronous copies; in the z forms ok == false fills zeros and reads nothing.
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "l"(policy)
@@ -124,11 +134,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void lds64(uint32_t& x, uint32_t& y, uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
 }
@@ -183,28 +188,32 @@ struct Tile {
   static constexpr int kRing = kWarps * kWarpBytes;
 };
 
-// Where a V row and its 16-byte pieces sit in a stage.  4-bit: lane t reads
-// keys 2t, 2t+1, 2t+8, 2t+9 of a block one after the other, so keys of the same
-// turn are neighbours; the pieces of every other row pair are exchanged so that
-// four rows of 64 bytes cover all banks.  bf16: ldmatrix reads one piece of 8 rows.
+// Where a V row and its 16-byte pieces sit in a stage: ldmatrix reads one piece of
+// 8 rows at a time, so the pieces change places from row to row.
 template <bool I4, int D>
 __device__ __forceinline__ int v_place(int key, int chunk) {
   if constexpr (I4) {
-    const int slot = (key & ~7) | ((key & 1) << 2) | ((key >> 1) & 3);
-    const int c = D == 128 ? chunk ^ (slot & 2) : chunk;
-    return slot * Tile<I4, D>::kRow + 16 * c;
+    return key * Tile<I4, D>::kRow + 16 * (D == 128 ? chunk ^ ((key >> 1) & 3) : chunk ^ ((key >> 2) & 1));
   } else {
     return key * Tile<I4, D>::kRow + 16 * (chunk ^ (key & 7));
   }
 }
-// K rows: bf16 swaps the 64-byte halves of odd rows (two rows a quarter warp).
+// K rows.  4-bit: the transposed bytes of V pair keys 4t, 4t + 2 and 4t + 1, 4t + 3 in
+// the value MMA, so rows g and g + 8 of a block's score MMA are keys 2g and 2g + 1:
+// the even keys of a block first, then the odd ones.  bf16: rows g and g + 8 are
+// keys g and g + 8, and the 64-byte halves of odd rows change places (two rows a
+// quarter warp).
 template <bool I4, int D>
 __device__ __forceinline__ int k_place(int key, int chunk) {
   if constexpr (I4) {
-    return key * Tile<I4, D>::kRow + 16 * chunk;
+    return ((key & ~15) | ((key & 1) << 3) | ((key >> 1) & 7)) * Tile<I4, D>::kRow + 16 * chunk;
   } else {
     return key * Tile<I4, D>::kRow + 16 * (chunk ^ ((key & 1) << 2));
   }
+}
+template <bool I4>
+__device__ __forceinline__ int key_of_row(int g, int r) {  // of row g + 8 r of a block
+  return I4 ? 2 * g + r : g + 8 * r;
 }
 
 // A lane's part of its warp's tile copies: 32 pieces of 16 bytes a step, so every
@@ -237,7 +246,8 @@ struct Loader {
       V += lane * 16;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        cp16(stage + kdst + 512 * i, K + 512 * i, policy);
+        // (4-bit, d = 128: eight keys a step, so the even and odd ones of half a block.)
+        cp16(stage + kdst + (I4 && D == 128 ? (i >> 1) * 1024 + (i & 1) * 256 : 512 * i), K + 512 * i, policy);
         if constexpr (I4) {
           cp16(stage + vdst + 512 * i, V + 512 * i, policy);
         } else {
@@ -460,15 +470,16 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
   constexpr int NT = Sc::NT, KS = D / 16, NB = kHalf ? 1 : Sc::NB;  // blocks this lane weighs
   const int g = lane >> 2, t = lane & 3;
   const bool second = kHalf && (t & G);
-  const int key0 = g + (second ? 16 : 0);
+  const int block0 = second ? 16 : 0;  // first key of this lane's block
   float sc[NB][NT][2], tt[NB][NT][2], sv[NB][2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < NB; ++b) {
+    uint32_t kv[4] = {};  // (K word, V word) of both keys
+    if constexpr (I4) lds128(kv, stage + T::kPOff + 8 * (block0 + 16 * b + 2 * g));
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int key = key0 + 16 * b + 8 * r;
-      uint32_t pk = 0u, pv = 0u;
-      if constexpr (I4) lds64(pk, pv, stage + T::kPOff + 8 * key);
+      const int key = block0 + 16 * b + key_of_row<I4>(g, r);
+      const uint32_t pk = kv[2 * r], pv = kv[2 * r + 1];
       sv[b][r] = I4 ? bf_lo(pv) : 1.f;
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
@@ -492,6 +503,7 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
         }
       }
     }
+  }
   if (j0 + T::kKeys > n) {  // keys behind the end
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -499,7 +511,7 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
       for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          if (j0 + key0 + 16 * b + 8 * r >= n) sc[b][u][r] = -CUDART_INF_F;
+          if (j0 + block0 + 16 * b + key_of_row<I4>(g, r) >= n) sc[b][u][r] = -CUDART_INF_F;
   }
   bool raise = false;
 #pragma unroll
@@ -568,37 +580,24 @@ __device__ __forceinline__ void value_block(State<D, (G + 3) / 4>& s, const Weig
     }
   };
   if constexpr (I4) {
-    constexpr int WPG = D / 64;  // code words a lane has of a key
-    uint32_t w[4][2], mz[2];
+    // Register r of a 16-byte piece: the bytes 8 r + g of keys 4t .. 4t + 3, so two
+    // neighbouring dims; their even keys' codes and (8 bits on) their odd keys'.
+    uint32_t kv[2][4], mz[2];  // (K word, V word) of four keys
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // Key 2t + (e & 1) + 8 (e >> 1); its slot (v_place) is 8 (e >> 1) + 4 (e & 1) + t.
-      const int slot = 8 * (e >> 1) + 4 * (e & 1) + t;
-      const uint32_t row = stage + T::kVOff + (16 * b + slot) * T::kRow;
-      if constexpr (WPG == 2) {
-        lds64(w[e][0], w[e][1], row + ((8 * g) ^ ((slot & 2) << 4)));
-      } else {
-        w[e][0] = lds32(row + 4 * g);
+    for (int e = 0; e < 2; ++e) lds128(kv[e], stage + T::kPOff + 8 * (16 * b + 4 * t + 2 * e));
+    mz[0] = neg_zero_points(__byte_perm(kv[0][1], kv[1][1], 0x7632));
+    mz[1] = neg_zero_points(__byte_perm(kv[0][3], kv[1][3], 0x7632));
+    const int key = 16 * b + (lane & 15);
+#pragma unroll
+    for (int c = 0; c < T::kChunks; c += 2) {
+      uint32_t w[4];
+      ldmatrix2_bytes_trans(w, stage + T::kVOff + v_place<I4, D>(key, c + (lane >> 4)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = w[e], y = w[e] >> 8;
+        mma(2 * c + e, nib_even(x, mz[0]), nib_odd(x, mz[0]), nib_even(y, mz[1]), nib_odd(y, mz[1]));
       }
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      uint32_t kv[4];  // (K word, V word) of two keys
-      lds128(kv, stage + T::kPOff + 8 * (16 * b + 2 * t + 8 * e));
-      mz[e] = neg_zero_points(__byte_perm(kv[1], kv[3], 0x7632));
-    }
-#pragma unroll
-    for (int i = 0; i < WPG; ++i)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t sel = half ? 0x7632 : 0x5410;
-        const uint32_t x = __byte_perm(w[0][i], w[1][i], sel), y = __byte_perm(w[2][i], w[3][i], sel);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const uint32_t x8 = p ? x >> 8 : x, y8 = p ? y >> 8 : y;
-          mma(4 * i + 2 * half + p, nib_even(x8, mz[0]), nib_odd(x8, mz[0]), nib_even(y8, mz[1]), nib_odd(y8, mz[1]));
-        }
-      }
   } else {
     // Matrices of ldmatrix: (dims 0-7 | 8-15 of the tile) x (keys 0-7 | 8-15).
     const int key = 16 * b + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
@@ -644,16 +643,13 @@ __device__ __forceinline__ void write_records(State<D, (G + 3) / 4>& s, const Qu
     if (t < G) {
       float* rec = recs + (4 * u + t) * R;
       if (g == 0) *reinterpret_cast<float4*>(rec) = make_float4(s.m[u], s.omega[u], s.T[u], 0.f);
-      if constexpr (I4) {  // a lane's dims are D / 8 neighbours
+      if constexpr (I4) {  // rows g, g + 8 of tile i: dims 16 i + 2 g, 16 i + 2 g + 1
 #pragma unroll
-        for (int i = 0; i < KS; i += 2) {
-          const int d0 = (D / 8) * g + 2 * i;
+        for (int i = 0; i < KS; ++i) {
           const float(&x)[4] = s.O[u][i];
-          const float(&y)[4] = s.O[u][i + 1];
-          *reinterpret_cast<float4*>(rec + 4 + d0) =
-              make_float4(x[0] * kUnit, x[2] * kUnit, y[0] * kUnit, y[2] * kUnit);
-          *reinterpret_cast<float4*>(rec + 4 + D + d0) =
-              make_float4(x[1] * (kUnit * f2), x[3] * (kUnit * f2), y[1] * (kUnit * f2), y[3] * (kUnit * f2));
+          *reinterpret_cast<float2*>(rec + 4 + 16 * i + 2 * g) = make_float2(x[0] * kUnit, x[2] * kUnit);
+          *reinterpret_cast<float2*>(rec + 4 + D + 16 * i + 2 * g) =
+              make_float2(x[1] * (kUnit * f2), x[3] * (kUnit * f2));
         }
       } else {
 #pragma unroll
