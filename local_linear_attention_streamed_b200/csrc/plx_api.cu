@@ -668,8 +668,18 @@ int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams
   return cuda_rc(launch_kv_append_int4(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// PLX_OK, or why the cache decodes refuse these sizes.
+static int check_cache_decode_sizes(int B, int H, int Hkv, int L, int d) {
+  if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0) return PLX_ERR_INVALID_ARG;
+  const int G = H / Hkv;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return PLX_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
+  return decode_sizes_supported(B, H, Hkv, L) ? PLX_OK : PLX_ERR_UNSUPPORTED;
+}
+
 static size_t cache_decode_bytes(int B, int H, int Hkv, int L, int d, bool int4, bool weights) {
-  if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0) return 0;
+  // The plan divides by what it derives from d and H / Hkv: only for sizes that the calls take.
+  if (check_cache_decode_sizes(B, H, Hkv, L, d) != PLX_OK) return 0;
   return cache_decode_space(B, H, Hkv, L, d, num_sms_or_default(), int4, weights).bytes;
 }
 
@@ -688,22 +698,18 @@ static int cache_decode_impl(const void* q, const void* r, const void* K, const 
                              size_t workspace_bytes, void* stream) {
   if (!q || !r || !K || !V || !seqlens || !out || (int4 && (!Kp || !Vp)) || (weights && (!w_in || !w_out)))
     return PLX_ERR_INVALID_ARG;
-  if (B < 1 || H < 1 || Hkv < 1 || L < 1 || d < 1 || H % Hkv != 0) return PLX_ERR_INVALID_ARG;
-  const int G = H / Hkv;
-  if (G != 1 && G != 2 && G != 4 && G != 8) return PLX_ERR_UNSUPPORTED;
-  if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
+  int rc = check_cache_decode_sizes(B, H, Hkv, L, d);
+  if (rc != PLX_OK) return rc;
   if (!aligned16(q) || !aligned16(r) || !aligned16(K) || !aligned16(V) || !aligned16(out) || !aligned4(seqlens) ||
       !aligned4(Kp) || !aligned4(Vp) || !aligned4(w_in) || !aligned4(w_out))
     return PLX_ERR_MISALIGNED;
-  if (!decode_sizes_supported(B, H, Hkv, L)) return PLX_ERR_UNSUPPORTED;
   if (weights && w_in != w_out) {  // the same array or apart
     const uintptr_t w0 = reinterpret_cast<uintptr_t>(w_in), w1 = reinterpret_cast<uintptr_t>(w_out);
     const size_t bytes = 4 * (size_t)B * Hkv * L;
     if (w0 < w1 + bytes && w1 < w0 + bytes) return PLX_ERR_INVALID_ARG;
   }
   DeviceCache* dc = nullptr;
-  int rc = current_device(&dc);
-  if (rc != PLX_OK) return rc;
+  if ((rc = current_device(&dc)) != PLX_OK) return rc;
   const CacheDecodeSpace need = cache_decode_space(B, H, Hkv, L, d, dc->num_sms, int4, weights);
   char* ws = static_cast<char*>(workspace);
   if (need.bytes > 0) {

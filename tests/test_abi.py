@@ -268,3 +268,25 @@ def test_cache_evict_rejects_bad_arguments(lib):
                 w=0x200000000, wo=0x300000000) == -2
     assert call(B=1 << 20, Hkv=32, w=0x20000000000, wo=0x30000000000) == -2
     assert call(w=0x2000002) == -3
+
+
+def test_cache_decode_size_queries_of_refused_sizes(lib):
+    """0 for every size that the calls refuse, a head size beyond 2048 among them (in a process of its own: a query
+    that divides by zero ends it)."""
+    import subprocess
+    import sys
+    refused = [(1, 1, 1, 64, 96), (1, 1, 1, 64, 2048), (1, 1, 1, 64, 2049), (1, 1, 1, 64, 4096), (2, 4, 1, 7, 1 << 24),
+               (1, 3, 1, 64, 128), (1, 16, 1, 64, 128), (1, 64, 1, 64, 64), (1 << 20, 32, 32, 64, 128),
+               (4, 64, 16, ((1 << 31) - 128) // 64, 128), ((1 << 31) - 1,) * 5, (1, 8, 0, 64, 128), (1, 8, 2, 0, 128)]
+    code = f"""
+import ctypes
+lib = ctypes.CDLL({os.path.join(PKG, 'libplx.so')!r})
+for name in ("plx_decode_int4kv_workspace_bytes", "plx_decode_weights_workspace_bytes"):
+    query = getattr(lib, name)
+    query.restype, query.argtypes = ctypes.c_size_t, [ctypes.c_int] * 5
+    for sizes in {refused!r}:
+        assert query(*sizes) == 0, (name, sizes)
+    assert query(1, 8, 2, 1 << 20, 128) > 0 and query(1, 1, 1, 1 << 20, 64) > 0
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, (done.returncode, done.stderr[-2000:])
