@@ -445,9 +445,10 @@ int plx_decode_int4kv_weights(const void* q, const void* r, const void* Kcodes, 
  * of rows of row_bytes[c] (1..65536) bytes: bf16, fp32, e4m3 or 4-bit rows, their
  * scales or params; caches_out [B, Hkv, L_out], L_out >= min(budget, L).  In
  * place: caches_out[c] = caches[c] or weights_out = weights, with L_out = L;
- * seqlens_out may be seqlens.  Other overlaps of an output with a cache, the
- * weights or another output give PLX_ERR_INVALID_ARG, as do
- * budget < 1, negative sinks or recent, and sinks + recent > budget.  A seqlens
+ * seqlens_out may be seqlens.  Other overlaps of an output (kept and seqlens_out
+ * among them) with a cache, the weights, seqlens or another output give
+ * PLX_ERR_INVALID_ARG, as do budget < 1, negative sinks or recent, and
+ * sinks + recent > budget.  A seqlens
  * entry outside 1..L keeps nothing (kept -1, weights_out 0, length 0, rows
  * untouched) and reports PLX_ERR_BAD_SEQLEN.  Two launches; no workspace.
  */

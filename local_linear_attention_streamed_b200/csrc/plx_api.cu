@@ -814,6 +814,20 @@ int plx_cache_evict(int count, const void* const* caches, void* const* caches_ou
   if (!aligned4(weights) || !aligned4(weights_out) || !aligned4(seqlens) || !aligned4(seqlens_out) ||
       !aligned4(kept))
     return PLX_ERR_MISALIGNED;
+  // The kernels read lengths, kept positions, rows and totals while they write: the
+  // positions and the lengths lie apart from everything else (the new lengths may
+  // be written over the old ones, of which min(n, budget) is all that is used then).
+  const uintptr_t n0 = reinterpret_cast<uintptr_t>(seqlens), n1 = n0 + 4 * (size_t)B;
+  const uintptr_t m0 = reinterpret_cast<uintptr_t>(seqlens_out), m1 = m0 + 4 * (size_t)B;
+  const uintptr_t k0 = reinterpret_cast<uintptr_t>(kept), k1 = k0 + 4 * (size_t)units * std::min(budget, L);
+  auto meet = [](uintptr_t x0, uintptr_t x1, uintptr_t y0, uintptr_t y1) { return x0 < y1 && y0 < x1; };
+  if (meet(k0, k1, n0, n1) || meet(k0, k1, m0, m1) || (n0 != m0 && meet(n0, n1, m0, m1))) return PLX_ERR_INVALID_ARG;
+  for (int c = 0; c <= count; ++c) {
+    const uintptr_t s0 = span[c][0], s1 = span[c][1], t0 = span[c][2], t1 = span[c][3];
+    if (meet(k0, k1, s0, s1) || meet(k0, k1, t0, t1) || meet(m0, m1, s0, s1) || meet(m0, m1, t0, t1) ||
+        meet(n0, n1, t0, t1))
+      return PLX_ERR_INVALID_ARG;
+  }
   DeviceCache* dc = nullptr;
   int rc = current_device(&dc);
   if (rc != PLX_OK) return rc;

@@ -290,3 +290,34 @@ for name in ("plx_decode_int4kv_workspace_bytes", "plx_decode_weights_workspace_
 """
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert done.returncode == 0, (done.returncode, done.stderr[-2000:])
+
+
+def test_cache_evict_rejects_overlaps_of_positions_and_lengths(lib):
+    """kept and seqlens_out are outputs too: apart from every cache, the totals, the lengths and each other."""
+    vp, it = ctypes.c_void_p, ctypes.c_int
+    B, Hkv, L, Lout, budget = 2, 2, 64, 16, 16
+    src, dst, w, wo = 0x1000000, 0x2000000, 0x3000000, 0x4000000      # 256-byte rows: 0x10000 and 0x4000 bytes
+    sl, slo, kept = 0x5000000, 0x6000000, 0x7000000                    # 8, 8 and 256 bytes
+
+    def call(**kw):
+        a = dict(src=src, dst=dst, w=w, wo=wo, sl=sl, slo=slo, kept=kept)
+        a.update(kw)
+        return lib.plx_cache_evict(1, (vp * 1)(a["src"]), (vp * 1)(a["dst"]), (it * 1)(256), a["w"], a["wo"], a["sl"],
+                                   a["slo"], a["kept"], B, Hkv, L, Lout, budget, 1, 2, None)
+
+    spans = dict(src=(src, 0x10000), dst=(dst, 0x4000), w=(w, B * Hkv * L * 4), wo=(wo, B * Hkv * Lout * 4),
+                 sl=(sl, 8), slo=(slo, 8), kept=(kept, 256))
+    for out in ("kept", "slo"):
+        for name, (at, size) in spans.items():
+            if name == out:
+                continue
+            for x in (at, at + size - 4, at - spans[out][1] + 4):
+                if out == "slo" and name == "sl" and x == at:
+                    continue  # new lengths over the old ones are allowed
+                assert call(**{out: x}) == -1, (out, name, hex(x))
+    for name in ("dst", "wo"):  # rows and totals written over the lengths that are read meanwhile
+        at, size = spans[name]
+        for x in (at, at + size - 4, at - 4):
+            assert call(sl=x) == -1, (name, hex(x))
+    assert call(sl=src + 64, slo=src + 64) == -1  # new lengths over the old ones, inside of a cache
+    assert call(sl=w, slo=w) == -1
