@@ -393,7 +393,8 @@ int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams
  * form).  q, r, out: bf16 [B, H, d]; codes uint8 [B, Hkv, L, d/2]; params bf16
  * [B, Hkv, L, 2]; seqlens int32 [B] in 1..L (others write zeros and report
  * PLX_ERR_BAD_SEQLEN).  Query head h reads KV head h / (H/Hkv), groups of 1, 2, 4
- * or 8; d in {64, 128}, else PLX_ERR_UNSUPPORTED.  Cache rows at and behind
+ * or 8; d in {64, 128}; B H <= 2^24, B Hkv L + 128 < 2^31, L <= 2^31 - 4096; else
+ * PLX_ERR_UNSUPPORTED (and a workspace size of 0).  Cache rows at and behind
  * seqlens[b] are not read.  It reads 2 (d/2 + 4) bytes a cached key.  Elements of
  * q and r up to 2^120 in magnitude are computed with; larger ones give infinities
  * or NaN.
@@ -443,7 +444,8 @@ int plx_decode_int4kv_weights(const void* q, const void* r, const void* Kcodes, 
  *   seqlens_out[b]     = min(seqlens[b], budget)
  * caches: HOST arrays of `count` (0..8) device pointers to tensors [B, Hkv, L]
  * of rows of row_bytes[c] (1..65536) bytes: bf16, fp32, e4m3 or 4-bit rows, their
- * scales or params; caches_out [B, Hkv, L_out], L_out >= min(budget, L).  In
+ * scales or params; caches_out [B, Hkv, L_out], L_out >= min(budget, L); B Hkv <=
+ * 2^24 and, for L and L_out, B Hkv L + 128 < 2^31, L <= 2^31 - 4096.  In
  * place: caches_out[c] = caches[c] or weights_out = weights, with L_out = L;
  * seqlens_out may be seqlens.  Other overlaps of an output (kept and seqlens_out
  * among them) with a cache, the weights, seqlens or another output give

@@ -674,7 +674,7 @@ static int check_cache_decode_sizes(int B, int H, int Hkv, int L, int d) {
   const int G = H / Hkv;
   if (G != 1 && G != 2 && G != 4 && G != 8) return PLX_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return PLX_ERR_UNSUPPORTED;
-  return decode_sizes_supported(B, H, Hkv, L) ? PLX_OK : PLX_ERR_UNSUPPORTED;
+  return decode_sizes_supported(B, H, Hkv, L) && L <= kMostCacheRows ? PLX_OK : PLX_ERR_UNSUPPORTED;
 }
 
 static size_t cache_decode_bytes(int B, int H, int Hkv, int L, int d, bool int4, bool weights) {
@@ -781,7 +781,8 @@ int plx_cache_evict(int count, const void* const* caches, void* const* caches_ou
       L_out < std::min(budget, L))
     return PLX_ERR_INVALID_ARG;
   if (count > kEvictMaxCaches) return PLX_ERR_UNSUPPORTED;
-  if (!decode_sizes_supported(B, Hkv, Hkv, L) || !decode_sizes_supported(B, Hkv, Hkv, L_out))
+  if (!decode_sizes_supported(B, Hkv, Hkv, L) || !decode_sizes_supported(B, Hkv, Hkv, L_out) ||
+      std::max(L, L_out) > kMostCacheRows)
     return PLX_ERR_UNSUPPORTED;
   EvictArgs a{};
   a.count = count;

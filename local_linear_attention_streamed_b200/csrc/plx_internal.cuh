@@ -139,6 +139,11 @@ inline bool decode_sizes_supported(int B, int H, int Hkv, int L) {
   return (long long)B * H <= (1ll << 24) && (long long)B * Hkv * L + 128 < (1ll << 31);
 }
 
+// Rows a sequence, of the cache decodes and the eviction: their kernels count in
+// int, up to 2047 past the last row (a block's turn of the selection, a run of keys
+// of the weights), and a wrapped index would count as a row to keep.
+constexpr int kMostCacheRows = 0x7fffffff - 4095;
+
 // bf16 causal/full prefill on tcgen05 + TMA + TMEM, d == 128.
 bool prefill_tc_supported(int d);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t st, int num_sms);

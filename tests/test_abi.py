@@ -321,3 +321,22 @@ def test_cache_evict_rejects_overlaps_of_positions_and_lengths(lib):
             assert call(sl=x) == -1, (name, hex(x))
     assert call(sl=src + 64, slo=src + 64) == -1  # new lengths over the old ones, inside of a cache
     assert call(sl=w, slo=w) == -1
+
+
+def test_cache_calls_refuse_lengths_next_to_2_31(lib):
+    """The kernels count rows in 32 bits, a block's turn past the last one."""
+    vp, it = ctypes.c_void_p, ctypes.c_int
+    most = (1 << 31) - 4096
+    far = [1 << 44, 2 << 44, 3 << 44, 4 << 44, 5 << 44, 6 << 44]
+    for L in (most + 1, (1 << 31) - 2047, (1 << 31) - 129):
+        for Lout in (16, L):
+            assert lib.plx_cache_evict(0, (vp * 1)(), (vp * 1)(), (it * 1)(), far[0], far[1], far[2], far[3], far[4],
+                                       1, 1, L, Lout, 16, 1, 2, None) == -2
+        assert lib.plx_cache_evict(0, (vp * 1)(), (vp * 1)(), (it * 1)(), far[0], far[1], far[2], far[3], far[4],
+                                   1, 1, 64, L, 16, 1, 2, None) == -2
+        tail = (1, 1, 1, L, 64, None, 0, None)
+        assert lib.plx_decode_weights(*far[:4], far[4], A, A + (1 << 40), far[5], *tail) == -2
+        assert lib.plx_decode_int4kv_weights(*far, A, A, A + (1 << 40), A, *tail) == -2
+        assert lib.plx_decode_int4kv(*far, A, A, *tail) == -2
+        assert lib.plx_decode_weights_workspace_bytes(1, 1, 1, L, 64) == 0
+    assert lib.plx_decode_weights_workspace_bytes(1, 1, 1, most, 64) > 4 * most
