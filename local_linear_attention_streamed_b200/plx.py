@@ -663,9 +663,10 @@ def cache_evict(caches, weights, seqlens, budget: int, sinks: int = 0, recent: i
         caches_out, weights_out = caches, weights
     if len(caches_out) != len(caches):
         raise ValueError("caches_out must hold one tensor for each of caches")
-    if max(budget, sinks, recent) >= 1 << 31:
-        raise ValueError("budget, sinks and recent must be below 2^31")
     index, (B, Hkv, L), L_out = weights.get_device(), weights.shape, weights_out.shape[-1]
+    # ctypes passes the low 32 bits of larger numbers.
+    if max(budget, sinks, recent, B, Hkv, L, L_out) >= 1 << 31 or min(budget, sinks, recent) < -(1 << 31):
+        raise ValueError("sizes, budget, sinks and recent must fit 32 bits")
     kept = torch.empty((B, Hkv, min(max(budget, 0), L)), dtype=_I32, device=index)
     if seqlens_out is None:
         seqlens_out = torch.empty((B,), dtype=_I32, device=index)
@@ -675,7 +676,7 @@ def cache_evict(caches, weights, seqlens, budget: int, sinks: int = 0, recent: i
         rest = t.shape[3:]
         src[i] = _ptr(t, "caches", (B, Hkv, L, *rest), t.dtype, index)
         dst[i] = _ptr(o, "caches_out", (B, Hkv, L_out, *rest), t.dtype, index)
-        row[i] = t.element_size() * math.prod(rest)
+        row[i] = min(t.element_size() * math.prod(rest), 1 << 30)  # (refused from 65537 on)
     rc = lib.plx_cache_evict(n, src, dst, row, _ptr(weights, "weights", (B, Hkv, L), _F32, index),
                              _ptr(weights_out, "weights_out", (B, Hkv, L_out), _F32, index),
                              _ptr(seqlens, "seqlens", (B,), _I32, index),

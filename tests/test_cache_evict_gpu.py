@@ -227,29 +227,3 @@ def test_refusals(plx):
         plx.cache_evict([t], wd, sl, 10, caches_out=[t])
     with pytest.raises(ValueError):
         plx.cache_evict([t], wd, sl, 10, caches_out=[], weights_out=wd)
-
-
-def test_neighbouring_buffers_are_not_overlaps(plx):
-    """Caches, totals and lengths cut out of one buffer, each ending where the next begins."""
-    B, Hkv, L, budget = 2, 2, 64, 16
-    w, caches = make(11, B, Hkv, L)
-    sizes = [B * Hkv * L * 256, B * Hkv * budget * 256, B * Hkv * L * 4, B * Hkv * budget * 4, B * 4, B * 4]
-    buf = torch.zeros(sum(sizes), dtype=torch.uint8, device="cuda")
-    at = [sum(sizes[:i]) for i in range(len(sizes))]
-    part = [buf[a:a + n] for a, n in zip(at, sizes)]
-    src, dst = (p.view(torch.bfloat16).view(B, Hkv, -1, 128) for p in part[:2])
-    wd, wo = (p.view(torch.float32).view(B, Hkv, -1) for p in part[2:4])
-    sl, new = (p.view(torch.int32) for p in part[4:])
-    src.copy_(caches[0]), wd.copy_(w), sl.copy_(torch.tensor([64, 40]))
-    kept, got = plx.cache_evict([src], wd, sl, budget, 1, 2, caches_out=[dst], weights_out=wo, seqlens_out=new)
-    assert got is new and new.tolist() == [16, 16] and sl.tolist() == [64, 40]
-    assert np.array_equal(raw(src), raw(caches[0])) and torch.equal(wd.cpu(), w)
-    for b, n in enumerate([64, 40]):
-        for h in range(Hkv):
-            ids = oracle.evict_ref(w[b, h].tolist(), n, budget, 1, 2)
-            assert kept[b, h].tolist() == ids.tolist()
-            assert np.array_equal(raw(dst)[b, h], raw(caches[0])[b, h, ids])
-            assert torch.equal(wo[b, h].cpu(), w[b, h, ids])
-    with pytest.raises(plx.PlxError):  # new lengths over the totals
-        plx.cache_evict([src], wd, sl, budget, 1, 2, caches_out=[dst], weights_out=wo,
-                        seqlens_out=wd.view(torch.int32).view(-1)[:B])

@@ -392,24 +392,6 @@ def test_binding_refuses(plx):
         plx.kv_quantize_int4(torch.zeros((4, 64), dtype=torch.bfloat16))
 
 
-@pytest.mark.parametrize("d", [32, 96, 2048, 2050, 4096])
-def test_unsupported_head_sizes_raise(plx, d):
-    """The binding asks for the workspace's size before the call checks the sizes."""
-    B, Hkv, L = 1, 2, 5
-    q = torch.zeros((B, Hkv, d), dtype=torch.bfloat16, device="cuda")
-    K = torch.zeros((B, Hkv, L, d), dtype=torch.bfloat16, device="cuda")
-    codes = torch.zeros((B, Hkv, L, d // 2), dtype=torch.uint8, device="cuda")
-    params = torch.zeros((B, Hkv, L, 2), dtype=torch.bfloat16, device="cuda")
-    w = torch.zeros((B, Hkv, L), device="cuda")
-    sl = torch.full((B,), L, dtype=torch.int32, device="cuda")
-    for call in (lambda: plx.decode_weights(q, q, K, K, sl, w),
-                 lambda: plx.decode_int4kv_weights(q, q, codes, params, codes, params, sl, w),
-                 lambda: plx.decode_int4kv(q, q, codes, params, codes, params, sl)):
-        with pytest.raises(plx.PlxError) as e:
-            call()
-        assert e.value.code == -2
-
-
 def test_two_streams_at_once(plx):
     """Calls on two streams share nothing, whatever the sizes."""
     sizes = [(1, 2, 4, 6000, 128), (2, 1, 1, 9000, 64)]
