@@ -10,7 +10,12 @@
 //
 // streamed with one running reference m: omega = sum w, T = sum w t,
 // O1 = sum w v, O2 = sum w t v with w = 2^(s log2 e - m), and
-// out = ((1 + T/omega) O1 - O2) / omega.
+// out = ((1 + T/omega) O1 - O2) / omega.  Taking one number off all t_j does not
+// change out, so T and O2 are sums over t_j - t0, t0 the mean of t over the first
+// tile that a warp weighs: with t far from 0 for all keys (a direction that they
+// share and the probe sees) out would else be the small difference of two large
+// sums whose weights keep 16 bits.  300 keys with t of 2^15 + N(0, 9): off by up to
+// 0.06 in outputs of 0.1 without, by their rounding with t0.
 //
 // Bound: HBM.  A key costs 2 (d/2 + 4) bytes (4-bit) or 4 d (bf16) and 8 d
 // flops per query head; at 4 bits and d = 128 the stream leaves an SM 5.8
@@ -280,6 +285,7 @@ template <int D, int NT>
 struct State {
   float O[NT][D / 16][4];  // rows: head dims; columns 2t, 2t+1: O1, O2 of lane t's head
   float m[NT], omega[NT], T[NT];
+  float t0[NT];  // T and O2 are sums over t - t0
 };
 
 // The query rows as MMA columns: column g is q (even) or rho (odd) of head g/2 of
@@ -382,7 +388,7 @@ __device__ __forceinline__ void begin_unit(const CacheDecodeArgs& a, Query<D, (G
 #pragma unroll
   for (int u = 0; u < (G + 3) / 4; ++u) {
     s.m[u] = kNoRef;
-    s.omega[u] = s.T[u] = 0.f;
+    s.omega[u] = s.T[u] = s.t0[u] = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -491,9 +497,11 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
         if constexpr (I4) {  // sums of raw codes: the zero point times the row's sum goes off
           const float z = bf_hi(pk), sk = bf_lo(pk);
           s1 = fmaf(-z, q.sum[u][0], s1) * (q.scale[u][0] * sk);
-          s2 = fmaf(-z, q.sum[u][1], s2) * sk;  // its power of two comes in write_records
+          // (t's power of two comes in write_records)
+          s2 = fmaf(fmaf(-z, q.sum[u][1], s2), sk, -s.t0[u]);
         } else {
           s1 *= q.cs;
+          s2 -= s.t0[u];
         }
         sc[b][u][r] = s1;
         tt[b][u][r] = s2;
@@ -519,16 +527,22 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
 #pragma unroll
     for (int b = 0; b < NB; ++b) raise |= sc[b][u][0] > s.m[u] || sc[b][u][1] > s.m[u];
   if (__any_sync(0xffffffffu, raise)) {
+    const float share = __fdividef(1.f, (float)min(T::kKeys, n - j0));
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-      float mx = sc[0][u][0];
+      float mx = sc[0][u][0], by = 0.f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1]));
-      if constexpr (kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G));
+      for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1])), by += tt[b][u][0] + tt[b][u][1];
+      if constexpr (kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G)), by += __shfl_xor_sync(0xffffffffu, by, G);
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int o = 4; o < 32; o <<= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o)), by += __shfl_xor_sync(0xffffffffu, by, o);
       const float m = mx > s.m[u] ? mx + kHeadroom : s.m[u];
       const float f = ex2(s.m[u] - m);
+      by = s.m[u] == kNoRef ? by * share : 0.f;  // the first tile of this state (keys behind the end: t is 0)
+      s.t0[u] += by;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) tt[b][u][0] -= by, tt[b][u][1] -= by;
       s.m[u] = m;
       s.omega[u] *= f;
       s.T[u] *= f;
@@ -610,7 +624,7 @@ __device__ __forceinline__ void value_block(State<D, (G + 3) / 4>& s, const Weig
   }
 }
 
-// A record: m, omega, T, unused, O1[D], O2[D].
+// A record: m, omega, T, t0, O1[D], O2[D]; T and O2 of t - t0.
 template <int D>
 constexpr int kRec = 2 * D + 4;
 
@@ -642,7 +656,7 @@ __device__ __forceinline__ void write_records(State<D, (G + 3) / 4>& s, const Qu
     }
     if (t < G) {
       float* rec = recs + (4 * u + t) * R;
-      if (g == 0) *reinterpret_cast<float4*>(rec) = make_float4(s.m[u], s.omega[u], s.T[u], 0.f);
+      if (g == 0) *reinterpret_cast<float4*>(rec) = make_float4(s.m[u], s.omega[u], s.T[u], s.t0[u] * f2);
       if constexpr (I4) {  // rows g, g + 8 of tile i: dims 16 i + 2 g, 16 i + 2 g + 1
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -921,17 +935,19 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
   for (int e = threadIdx.x; e < G * D; e += kThreads) {
     const int h = e / D, dim = e % D;
     float m = recs[h * R];
+    const float t0 = recs[h * R + 3];  // (where the first warp has no tile, none has)
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) m = fmaxf(m, recs[(w * G + h) * R]);
     float omega = 0.f, tsum = 0.f, o1 = 0.f, o2 = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float* rec = recs + (w * G + h) * R;
-      const float f = ex2(rec[0] - m);
-      omega += f * rec[1];
-      tsum += f * rec[2];
+      const float4 x = *reinterpret_cast<const float4*>(rec);
+      const float f = ex2(x.x - m), by = x.w - t0;
+      omega += f * x.y;
+      tsum += f * fmaf(by, x.y, x.z);
       o1 += f * rec[4 + dim];
-      o2 += f * rec[4 + D + dim];
+      o2 += f * fmaf(by, rec[4 + dim], rec[4 + D + dim]);
     }
     if (a.splits == 1) {
       const float inv = 1.f / omega;
@@ -943,6 +959,7 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
         rec[0] = m;
         rec[1] = omega;
         rec[2] = tsum;
+        rec[3] = t0;
       }
       rec[4 + dim] = o1;
       rec[4 + D + dim] = o2;
@@ -954,15 +971,17 @@ __global__ void __launch_bounds__(kThreads, G == 8 ? 3 : 4) cache_decode_kernel(
   for (int e = split * kThreads + threadIdx.x; e < G * D; e += a.splits * kThreads) {
     const int h = e / D, dim = e % D;
     float m = kNoRef;
+    const float t0 = cluster.map_shared_rank(merged, a.splits - 1)[h * R + 3];  // the last CTA always has a tile
     for (int c = 0; c < a.splits; ++c) m = fmaxf(m, cluster.map_shared_rank(merged, c)[h * R]);
     float omega = 0.f, tsum = 0.f, o1 = 0.f, o2 = 0.f;
     for (int c = 0; c < a.splits; ++c) {
       const float* rec = cluster.map_shared_rank(merged, c) + h * R;
-      const float f = ex2(rec[0] - m);
-      omega += f * rec[1];
-      tsum += f * rec[2];
+      const float4 x = *reinterpret_cast<const float4*>(rec);
+      const float f = ex2(x.x - m), by = x.w - t0;
+      omega += f * x.y;
+      tsum += f * fmaf(by, x.y, x.z);
       o1 += f * rec[4 + dim];
-      o2 += f * rec[4 + D + dim];
+      o2 += f * fmaf(by, rec[4 + dim], rec[4 + D + dim]);
     }
     const float inv = 1.f / omega;
     out[e] = __float2bfloat16(((1.f + tsum * inv) * o1 - o2) * inv);
@@ -994,18 +1013,20 @@ struct Merge {
     const int dl = threadIdx.x % kLanes, grp = threadIdx.x / kLanes % kGroups, hp = threadIdx.x / (kLanes * kGroups);
     float4 x1 = make_float4(0.f, 0.f, 0.f, 0.f), x2 = x1;
     float m = kNoRef, omega = 0.f, tsum = 0.f;
+    // The first record's t0 for all of them.
+    const float t0 = a.records[((size_t)p.slot(p.c0) * G + h0 + hp) * R + 3];
 #pragma unroll 4
     for (int c = p.c0 + grp; c <= p.c1; c += kGroups) {
       const float4* rec = reinterpret_cast<const float4*>(a.records + ((size_t)p.slot(c) * G + h0 + hp) * R);
       const float4 x = rec[0], y1 = rec[1 + dl], y2 = rec[1 + kLanes + dl];
-      const float top = fmaxf(m, x.x), f0 = ex2(m - top), f = ex2(x.x - top);
+      const float top = fmaxf(m, x.x), f0 = ex2(m - top), f = ex2(x.x - top), by = x.w - t0;
       m = top;
       omega = f0 * omega + f * x.y;
-      tsum = f0 * tsum + f * x.z;
+      tsum = f0 * tsum + f * fmaf(by, x.y, x.z);
       x1.x = f0 * x1.x + f * y1.x, x1.y = f0 * x1.y + f * y1.y;
       x1.z = f0 * x1.z + f * y1.z, x1.w = f0 * x1.w + f * y1.w;
-      x2.x = f0 * x2.x + f * y2.x, x2.y = f0 * x2.y + f * y2.y;
-      x2.z = f0 * x2.z + f * y2.z, x2.w = f0 * x2.w + f * y2.w;
+      x2.x = f0 * x2.x + f * fmaf(by, y1.x, y2.x), x2.y = f0 * x2.y + f * fmaf(by, y1.y, y2.y);
+      x2.z = f0 * x2.z + f * fmaf(by, y1.z, y2.z), x2.w = f0 * x2.w + f * fmaf(by, y1.w, y2.w);
     }
     o1[threadIdx.x] = x1;
     o2[threadIdx.x] = x2;

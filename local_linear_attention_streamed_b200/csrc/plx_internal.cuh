@@ -236,7 +236,7 @@ struct CacheDecodeArgs {
   int splits;     // CTAs (a cluster) a (b, KV head), where shares is 0
   int shares;     // equal shares of all tiles, one warp each
   bool once;      // the cache is too large to stay in L2 until the next step
-  float* records; // [B*Hkv + shares, G, 2d + 4] fp32: m, omega, T, pad, O1[d], O2[d]
+  float* records; // [B*Hkv + shares, G, 2d + 4] fp32: m, omega, T, t0, O1[d], O2[d]
   int2* parts;    // [B*Hkv]: first and last share of every (b, KV head), -1 for a bad length
   float2* stats;  // [B*H]: m and omega of a head that one CTA finished (weights only)
   float* scores;  // log2-domain scores [B*Hkv, L, G] (weights only)

@@ -303,6 +303,58 @@ def test_large_scores(plx, G, d, rising, scale_v):
         check_weights(wo, q64, r64, K64, V64, lens, w, w)
 
 
+def spread(q, r, K, V, seqlens):
+    """sum_j p_j (1 + |t_j - tbar|) |v_j|: what rounding errors of the terms p_j (1 - (t_j - tbar)) v_j scale with."""
+    B, H, d = q.shape
+    G = H // K.shape[1]
+    out = np.zeros((B, H, d))
+    for b in range(B):
+        n = int(seqlens[b])
+        for h in range(H):
+            k, v = K[b, h // G, :n], V[b, h // G, :n]
+            p = oracle.softmax_weights_row(q[b, h], k)
+            t = k @ r[b, h]
+            out[b, h] = (p * (1 + np.abs(t - p @ t))) @ np.abs(v)
+    return out
+
+
+@pytest.mark.parametrize("B,Hkv,G,L,d", [
+    (2, 2, 1, 300, 128), (2, 1, 2, 300, 64), (2, 2, 4, 100, 128), (1, 2, 8, 2000, 64), (1, 1, 1, 17000, 64),
+    (1, 1, 4, 17000, 128), (300, 3, 1, 20, 64), (1, 2, 2, 1500, 128), (900, 1, 2, 33, 128),
+])
+@pytest.mark.parametrize("common", [2.0 ** 15, -2.0 ** 12, 0.0])
+def test_a_direction_that_all_keys_share(plx, B, Hkv, G, L, d, common):
+    """t = rho.k is about `common` for every key, with differences of a few units between them.
+
+    Taking one number off all t changes nothing in the formula, so errors may scale with the differences alone:
+    |g - o| <= 2^-8 |o| + 2^-13 sum p (1 + |t - tbar|) |v|.  Keys are integers -7..8 and the probe multiples of 1/8, so
+    t is exact in fp32 (multiples of 1/8 below 2^17); t less its reference and the sums over it are then rounded
+    relative to the differences: 2^-16 (bf16 pairs) and a few 2^-23, as in check_out."""
+    g = torch.Generator().manual_seed(L + G)
+    H = Hkv * G
+    K, V = whole_rows(g, B, Hkv, L, d), torch.randn((B, Hkv, L, d), generator=g)
+    K[..., :8] = 8
+    q = 0.05 * torch.randn((B, H, d), generator=g)
+    r = torch.randint(-2, 3, (B, H, d), generator=g).double() / 8
+    r[..., :8] = common / 64
+    q, r, K, V = (x.to(torch.bfloat16) for x in (q, r, K, V))
+    lens = torch.randint(1, L + 1, (B,), generator=g).tolist()
+    lens[0] = L
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    Kc, Kp, K4 = quantised(plx, K)
+    Vc, Vp, V4 = quantised(plx, V)
+    assert np.array_equal(K4, f64(K))
+    q64, r64, K64, w = f64(q), f64(r), f64(K), torch.zeros((B, Hkv, L), device="cuda")
+    qd, rd = q.cuda(), r.cuda()
+    outs = ((plx.decode_int4kv(qd, rd, Kc, Kp, Vc, Vp, sl), V4),
+            (plx.decode_int4kv_weights(qd, rd, Kc, Kp, Vc, Vp, sl, w), V4),
+            (plx.decode_weights(qd, rd, K.cuda(), V.cuda(), sl, w), f64(V)))
+    for out, V64 in outs:
+        want = oracle.decode_gqa_ref(q64, r64, K64, V64, lens)
+        err = np.abs(f64(out) - want) - 2.0 ** -8 * np.abs(want) - 2.0 ** -13 * spread(q64, r64, K64, V64, lens)
+        assert err.max() <= 0, err.max()
+
+
 def test_two_graphs_at_once_with_their_inputs_held(plx):
     """Captured decodes and evictions of two sizes, replayed on two streams at the same time, eager calls on a third;
     every tensor that a graph reads lives as long as the graph."""
