@@ -32,7 +32,8 @@
  * Memory and ownership: every tensor pointer is a DEVICE pointer owned by the
  * caller; the library keeps no reference after the call returns.  Calls are
  * asynchronous on the given CUDA stream (void* stands for cudaStream_t; NULL is
- * the legacy default stream).  All tensor pointers must be 16-byte aligned.
+ * the legacy default stream).  Outputs and workspaces do not overlap each other or
+ * an input, except where an entry point says so.  All tensor pointers must be 16-byte aligned.
  *
  * Errors: every entry point returns PLX_OK (0) or a negative code.  Argument
  * errors are detected on the host before anything is launched.  Errors found by
@@ -397,7 +398,9 @@ int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams
  * PLX_ERR_UNSUPPORTED (and a workspace size of 0).  Cache rows at and behind
  * seqlens[b] are not read.  It reads 2 (d/2 + 4) bytes a cached key.  Elements of
  * q and r up to 2^120 in magnitude are computed with; larger ones give infinities
- * or NaN.
+ * or NaN.  Scores, statistics and sums are fp32; the weights p and p t enter the
+ * value sums as pairs of bf16 numbers (2^-16 relative, as in the other decodes), t
+ * less its mean over the first keys.
  * workspace: plx_decode_int4kv_workspace_bytes() bytes, 256-byte aligned, no
  * initial contents; NULL is allowed where that is 0, else PLX_ERR_WORKSPACE.
  * Nothing else is shared between calls: calls with different workspaces may run
@@ -413,10 +416,10 @@ int plx_decode_int4kv(const void* q, const void* r, const void* Kcodes, const vo
  * cache) or plx_decode_int4kv (4-bit cache), and for every visible key j
  *   weights_out[b,g,j] = weights[b,g,j] + sum over the heads h of KV head g of p_hj,
  * p the softmax weights (rainbus.top summary, "Softmax Attention"), all fp32
- * [B, Hkv, L].  weights_out may be weights (running totals over the steps), any
- * other overlap gives PLX_ERR_INVALID_ARG; its entries at and behind seqlens[b], and those of a sequence whose seqlens entry
- * is outside 1..L, are left as they were.  A new key's entry has to be 0 before
- * its first step.  bf16 caches [B, Hkv, L, d].  workspace:
+ * [B, Hkv, L].  weights_out may be weights (running totals over the steps); where
+ * the two overlap in part the call gives PLX_ERR_INVALID_ARG.  Entries at and behind
+ * seqlens[b], and those of a sequence whose seqlens entry is outside 1..L, are left
+ * as they were.  A new key's entry has to be 0 before its first step.  bf16 caches [B, Hkv, L, d].  workspace:
  * plx_decode_weights_workspace_bytes() bytes (partial records and one fp32 score
  * for each query head and key), 256-byte aligned, no initial contents, required
  * (else PLX_ERR_WORKSPACE).  Sizes, alignment and independence of calls as

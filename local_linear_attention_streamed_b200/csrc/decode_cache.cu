@@ -49,11 +49,12 @@
 // workspace that a second kernel merges.  There are no counters and no
 // library-owned memory: calls on several streams are independent.
 //
-// What bounds it now: instructions.  14.5 a key and warp at G = 1, d = 128, 17 at
-// G = 4 (issue slots 60 % and 55 % busy, the ALU pipe 58 % and 47 %, the MMA pipe
-// 34 % and 37 %; 12 or 20 warps an SM in place of 16 change nothing or lose).  64 x
-// 16 sequences of 4096 keys: 95 us, 6.0 TB/s, 0.92 of a copy's rate, on a rested
-// GPU; 105 to 112 us at the clock that a long run keeps.
+// What bounds it now: instructions.  14.6 a key and warp at G = 1, d = 128, 17 at
+// G = 4 (issue slots 60 % and 55 % busy, the ALU pipe 59 % and 46 %, the MMA pipe
+// 34 % and 38 %; 12 or 20 warps an SM in place of 16 change nothing or lose).  64 x
+// 16 sequences of 4096 keys, one row appended to each before: 101 to 104 us on a
+// rested GPU, 115 to 118 us at the clock that a long run keeps: 0.87 and 0.75 of a
+// copy's rate.
 #include "launch.cuh"
 #include "plx_internal.cuh"
 
@@ -533,7 +534,10 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
       float mx = sc[0][u][0], by = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1])), by += tt[b][u][0] + tt[b][u][1];
-      if constexpr (kHalf) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G)), by += __shfl_xor_sync(0xffffffffu, by, G);
+      if constexpr (kHalf) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G));
+        by += __shfl_xor_sync(0xffffffffu, by, G);
+      }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1)
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o)), by += __shfl_xor_sync(0xffffffffu, by, o);
@@ -1207,17 +1211,32 @@ cudaError_t pick(const CacheDecodeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// How the keys are cut, by sizes alone.  Measured on a B200 with 4-bit rows, d =
-// 128, us with shares / one CTA a (b, KV head) / the best cluster of 2 to 8:
-//   many (b, KV head) balance themselves:   64 x 16 of 4096 keys           111 / 104 / 111
-//   (not where they are ragged:             64 x 16 of 2048..4096           86 /  92 /  92)
-//   fewer need shares:                      64 x 8 of 2048..4096, G = 4     57 /  64 /  68
-//                                           1 x 8 of 32768, G = 4           27 / 191 /  35
-//                                           1 x 2 of 32768                  18 / 188 /  35
-//   little work ends soonest in one launch: 8 x 8 of 2048..4096, G = 4      24 /  33 /  20
-//                                           1 x 2 of 4096, G = 4            12 /  30 /  12
-// (each includes about 8 us of an empty graph launch).
-// Weights take a second launch in any case, so only many units go without shares.
+// How the keys are cut, by sizes alone.  Measured on a B200, us a step (4-bit: with
+// the append before it) in a row of 20, with shares / one CTA a (b, KV head) / the
+// best cluster of 2 to 8; * is what the rule takes:
+//   4-bit rows                                               d = 128                  d = 64
+//   many (b, KV head) balance      64 x 16 of 4096           108 / 104* / 110         69 / 64* / 67
+//   (less so where ragged)         64 x 16 of 2048..4096      81 /  89* /  92         55 / 60* / 59
+//   fewer need shares              64 x 8 of 2048..4096, G 4  53* /  59 /  63         35* / 39 / 41
+//                                  80 x 8 of 1024..2048, G 8  59* /  63 /  73         36* / 38 / 44
+//                                  1 x 8 of 32768, G 4        20* / 175 /  29         14* / 110 / 19
+//                                  1 x 2 of 32768             13* / 149 /  24         10* /  97 / 17
+//   little work ends soonest       8 x 8 of 1024..2048, G 4   14  /  15 / 12.4* (4: 11.4)   11.5 / 10.5 / 8.8*
+//   in one launch                  1 x 2 of 4096, G 4        9.4  /  27 / 9.5*              7.8 / 17.6 / 7.3*
+//   the limit of 28 MB             2 x 8 of 8192 (17 MB)     15.2 /  41 / 13.3*
+//                                  2 x 8 of 12288 (26 MB)    15.5 /  59 / 16.6*
+//                                  2 x 8 of 16384 (34 MB)    17.4* /  77 / 19.8
+//                                  8 x 8 of 2048..4096, G 4 (34 MB)  17.2* / 26 / 15.1
+// Weights take a second launch in any case, so only many units go without shares:
+//   4-bit, shares / one CTA        64 x 8 of 2048..4096, G 4  61* /  73               42* / 49
+//                                  110 x 8 of 512..1024       28* /  30               22* / 20
+//                                  128 x 8 of 512..1024       32  /  32*              26  / 23*
+//   bf16                           64 x 8 of 2048..4096, G 4 138* / 140               75* / 76
+//                                  110 x 8 of 512..1024       58* /  57               36* / 33
+//                                  128 x 8 of 512..1024       67  /  65*              41  / 39*
+//                                  8 x 8 of 1024..2048, G 4  19.5* / 19.1            12.9* / 11.3
+// The rule's slots are of the 4-bit kernels: the bf16 ring lets two CTAs an SM run at
+// once, so half of the shares wait for the others there.
 CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num_sms, bool int4, bool weights) {
   CacheDecodeSpace w;
   const long long units = (long long)B * Hkv, slots = (H / Hkv == 8 ? 3ll : 4ll) * num_sms;
@@ -1236,7 +1255,10 @@ CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num
     return here;
   };
   if (flat) {
-    // A tile for every warp, and at most 256 records to merge for a (b, KV head) of L keys.
+    // A tile for every warp, and 256 records to merge for a (b, KV head), on average.
+    // Shares are dealt by the tiles that there are, so one long sequence among hundreds
+    // of short ones gets nearly all of them: 40000 keys beside 511 x 1..3 keys, d = 64,
+    // 1250 records and 96 us, 9 us alone.
     const long long warps = tiles < 256 * units ? tiles : 256 * units;
     w.shares = kWarps * (int)((warps + kWarps - 1) / kWarps < slots ? (warps + kWarps - 1) / kWarps : slots);
     w.records = take(sizeof(float) * (size_t)(units + w.shares) * (H / Hkv) * (2 * d + 4));
@@ -1249,7 +1271,8 @@ CacheDecodeSpace cache_decode_space(int B, int H, int Hkv, int L, int d, int num
   w.bytes = at;
   // Rows that will have left L2 before the next step reads them again need not stay
   // there: scores, records and what others keep stay instead (bf16 batch of 64 x 8 x
-  // 2048..4096 keys with weights: 145 -> 133 us).
+  // 2048..4096 keys with weights: 145 -> 133 us).  By the capacity: the lengths are on
+  // the device, and a large cache with few rows gives up its stay in L2.
   w.once = bytes > (96ll << 20);
   return w;
 }

@@ -27,7 +27,7 @@
 //
 // Bound: HBM.  2 d bytes of bf16 and d/2 + 4 bytes of codes and word a row; a
 // division an element would cost more than the stream (84 us for 8 x 16 x 4096
-// rows of 128, where this takes 33).
+// rows of 128, where this takes 29).
 #include "launch.cuh"
 #include "plx_internal.cuh"
 

@@ -136,7 +136,8 @@ def random_case(seed, B, Hkv, G, L, d):
         x = torch.randn(shape, generator=g)
         return x / x.square().mean(-1, keepdim=True).sqrt()
 
-    return dict(q=(1.5 * rms(B, H, d)).to(torch.bfloat16), r=(0.25 * torch.randn((B, H, d), generator=g)).to(torch.bfloat16),
+    return dict(q=(1.5 * rms(B, H, d)).to(torch.bfloat16),
+                r=(0.25 * torch.randn((B, H, d), generator=g)).to(torch.bfloat16),
                 K=rms(B, Hkv, L, d).to(torch.bfloat16), V=torch.randn((B, Hkv, L, d), generator=g).to(torch.bfloat16),
                 w=torch.rand((B, Hkv, L), generator=g), g=g)
 
