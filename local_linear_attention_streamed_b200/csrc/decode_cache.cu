@@ -533,7 +533,11 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
     for (int u = 0; u < NT; ++u) {
       float mx = sc[0][u][0], by = 0.f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1])), by += tt[b][u][0] + tt[b][u][1];
+      for (int b = 0; b < NB; ++b) {
+        mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1]));
+        by = fmaf(tt[b][u][0], share, by);  // (a sum of large t would pass fp32's range)
+        by = fmaf(tt[b][u][1], share, by);
+      }
       if constexpr (kHalf) {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G));
         by += __shfl_xor_sync(0xffffffffu, by, G);
@@ -543,7 +547,7 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o)), by += __shfl_xor_sync(0xffffffffu, by, o);
       const float m = mx > s.m[u] ? mx + kHeadroom : s.m[u];
       const float f = ex2(s.m[u] - m);
-      by = s.m[u] == kNoRef ? by * share : 0.f;  // the first tile of this state (keys behind the end: t is 0)
+      by = s.m[u] == kNoRef ? by : 0.f;  // the first tile of this state (keys behind the end: t is 0)
       s.t0[u] += by;
 #pragma unroll
       for (int b = 0; b < NB; ++b) tt[b][u][0] -= by, tt[b][u][1] -= by;

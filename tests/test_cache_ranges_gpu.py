@@ -356,6 +356,41 @@ def test_a_direction_that_all_keys_share(plx, B, Hkv, G, L, d, common):
         assert err.max() <= 0, err.max()
 
 
+@pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 64)])
+@pytest.mark.parametrize("scale", [2.0 ** 119, 2.0 ** -110])
+@pytest.mark.parametrize("int4", [False])
+def test_probes_of_extreme_size(plx, G, d, scale, int4):
+    """Probes next to 2^120, the largest that is computed with, and tiny ones.  t, about 2^6 scale for every key, is an
+    integer times scale / 4, and exact; a sum of 32 of the large ones passes fp32's range.  Values are 2^-20 where t is
+    large, so that outputs are bf16 numbers.  Bounds as in test_a_direction_that_all_keys_share."""
+    B, Hkv, L = 2, 2, 300
+    g = torch.Generator().manual_seed(G + d)
+    H = Hkv * G
+    K, V = whole_rows(g, B, Hkv, L, d), torch.randn((B, Hkv, L, d), generator=g) * min(1.0, 2.0 ** 99 / scale)
+    K[..., :8] = 8
+    q = 0.05 * torch.randn((B, H, d), generator=g)
+    r = torch.zeros((B, H, d), dtype=torch.float64)
+    r[..., 8:-2] = torch.randint(-1, 2, (B, H, d - 10), generator=g).double() / 4
+    r[..., :8] = 1
+    q, r, K, V = (x.to(torch.bfloat16) for x in (q, r * scale, K, V))
+    lens = [L, 77]
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qd, rd, w = q.cuda(), r.cuda(), torch.zeros((B, Hkv, L), device="cuda")
+    if int4:
+        Kc, Kp, K64 = quantised(plx, K)
+        Vc, Vp, V64 = quantised(plx, V)
+        assert np.array_equal(K64, f64(K))
+        outs = [plx.decode_int4kv(qd, rd, Kc, Kp, Vc, Vp, sl), plx.decode_int4kv_weights(qd, rd, Kc, Kp, Vc, Vp, sl, w)]
+    else:
+        K64, V64 = f64(K), f64(V)
+        outs = [plx.decode_weights(qd, rd, K.cuda(), V.cuda(), sl, w)]
+    want = oracle.decode_gqa_ref(f64(q), f64(r), K64, V64, lens)
+    allowed = 2.0 ** -8 * np.abs(want) + 2.0 ** -13 * spread(f64(q), f64(r), K64, V64, lens)
+    for out in outs:
+        err = np.abs(f64(out) - want) - allowed
+        assert err.max() <= 0, err.max()
+
+
 def test_two_graphs_at_once_with_their_inputs_held(plx):
     """Captured decodes and evictions of two sizes, replayed on two streams at the same time, eager calls on a third;
     every tensor that a graph reads lives as long as the graph."""
