@@ -671,7 +671,7 @@ __device__ __forceinline__ void write_records(State<D, (G + 3) / 4>& s, const Qu
           const float(&x)[4] = s.O[u][i];
           *reinterpret_cast<float2*>(rec + 4 + 16 * i + 2 * g) = make_float2(x[0] * kUnit, x[2] * kUnit);
           *reinterpret_cast<float2*>(rec + 4 + D + 16 * i + 2 * g) =
-              make_float2(x[1] * (kUnit * f2), x[3] * (kUnit * f2));
+              make_float2(x[1] * kUnit * f2, x[3] * kUnit * f2);  // (2^6 2^(7 + E) may pass fp32's range)
         }
       } else {
 #pragma unroll

@@ -358,7 +358,7 @@ def test_a_direction_that_all_keys_share(plx, B, Hkv, G, L, d, common):
 
 @pytest.mark.parametrize("G,d", [(1, 128), (2, 64), (4, 128), (8, 64)])
 @pytest.mark.parametrize("scale", [2.0 ** 119, 2.0 ** -110])
-@pytest.mark.parametrize("int4", [False])
+@pytest.mark.parametrize("int4", [True, False])
 def test_probes_of_extreme_size(plx, G, d, scale, int4):
     """Probes next to 2^120, the largest that is computed with, and tiny ones.  t, about 2^6 scale for every key, is an
     integer times scale / 4, and exact; a sum of 32 of the large ones passes fp32's range.  Values are 2^-20 where t is
