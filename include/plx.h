@@ -400,8 +400,8 @@ int plx_kv_append_int4(const void* k, const void* v, void* Kcodes, void* Kparams
  * q and r up to 2^120 in magnitude are computed with; larger ones give infinities
  * or NaN.  Scores, statistics and sums are fp32; the weights p and p t enter the
  * value sums as pairs of bf16 numbers (2^-16 relative, as in the other decodes), t
- * less its mean over the first keys.  Terms w s_V and w t s_K s_V / max|r| (s: the
- * rows' scales) keep their bits between 2^-117 and 2^127.
+ * less its mean over the first keys.  Over 4-bit rows p s and
+ * p t s / max|r| (s: a value row's scale) keep their bits from 2^-117 to 2^127.
  * workspace: plx_decode_int4kv_workspace_bytes() bytes, 256-byte aligned, no
  * initial contents; NULL is allowed where that is 0, else PLX_ERR_WORKSPACE.
  * Nothing else is shared between calls: calls with different workspaces may run

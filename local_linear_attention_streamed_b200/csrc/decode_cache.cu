@@ -528,15 +528,14 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
 #pragma unroll
     for (int b = 0; b < NB; ++b) raise |= sc[b][u][0] > s.m[u] || sc[b][u][1] > s.m[u];
   if (__any_sync(0xffffffffu, raise)) {
-    const float share = __fdividef(1.f, (float)min(T::kKeys, n - j0));
+    const float share = __fdividef(32.f, (float)min(T::kKeys, n - j0));
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       float mx = sc[0][u][0], by = 0.f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         mx = fmaxf(mx, fmaxf(sc[b][u][0], sc[b][u][1]));
-        by = fmaf(tt[b][u][0], share, by);  // (a sum of large t would pass fp32's range)
-        by = fmaf(tt[b][u][1], share, by);
+        by += (tt[b][u][0] + tt[b][u][1]) * (1.f / 32);  // (a sum of large t would pass fp32's range)
       }
       if constexpr (kHalf) {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, G));
@@ -547,7 +546,7 @@ __device__ __forceinline__ void weigh_tile(State<D, (G + 3) / 4>& s, Weights<I4,
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o)), by += __shfl_xor_sync(0xffffffffu, by, o);
       const float m = mx > s.m[u] ? mx + kHeadroom : s.m[u];
       const float f = ex2(s.m[u] - m);
-      by = s.m[u] == kNoRef ? by : 0.f;  // the first tile of this state (keys behind the end: t is 0)
+      by = s.m[u] == kNoRef ? by * share : 0.f;  // the first tile of this state (keys behind the end: t is 0)
       s.t0[u] += by;
 #pragma unroll
       for (int b = 0; b < NB; ++b) tt[b][u][0] -= by, tt[b][u][1] -= by;
@@ -671,7 +670,7 @@ __device__ __forceinline__ void write_records(State<D, (G + 3) / 4>& s, const Qu
           const float(&x)[4] = s.O[u][i];
           *reinterpret_cast<float2*>(rec + 4 + 16 * i + 2 * g) = make_float2(x[0] * kUnit, x[2] * kUnit);
           *reinterpret_cast<float2*>(rec + 4 + D + 16 * i + 2 * g) =
-              make_float2(x[1] * kUnit * f2, x[3] * kUnit * f2);  // (2^6 2^(7 + E) may pass fp32's range)
+              make_float2(x[1] * f2 * kUnit, x[3] * f2 * kUnit);  // (2^6 2^(7 + E) may pass fp32's range)
         }
       } else {
 #pragma unroll
