@@ -96,6 +96,31 @@ def test_neighbouring_buffers_are_not_overlaps(plx):
                         seqlens_out=wd.view(torch.int32).view(-1)[:B])
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_eviction_beyond_32_bit_offsets(plx, in_place):
+    """Rows of the second head lie more than 2^32 bytes into their cache, and kept ones up to its end."""
+    L, budget, sinks, recent = 70_000_000, 5000, 3, 60
+    cache = torch.empty((1, 2, L, 64), dtype=torch.uint8, device="cuda")
+    w = torch.rand((1, 2, L), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    heavy = torch.stack([torch.randperm(L - recent - sinks, generator=g, device="cuda")[:budget - sinks - recent]
+                         for _ in range(2)]).sort(-1).values + sinks
+    w.scatter_(2, heavy[None], 2.0 + torch.rand(heavy.shape, generator=g, device="cuda")[None])
+    ends = torch.arange(sinks, device="cuda"), torch.arange(L - recent, L, device="cuda")
+    want = torch.stack([torch.cat((ends[0], h, ends[1])) for h in heavy])
+    rows = torch.randint(0, 256, (2, budget, 64), generator=g, device="cuda", dtype=torch.uint8)
+    for h in range(2):
+        cache[0, h, want[h]] = rows[h]
+    totals = torch.gather(w[0], 1, want)
+    to, w_to = (cache, w) if in_place else (torch.empty_like(cache[:, :, :budget]), torch.empty_like(w[:, :, :budget]))
+    sl = torch.tensor([L], dtype=torch.int32, device="cuda")
+    kept, new = plx.cache_evict([cache], w, sl, budget, sinks, recent, caches_out=[to], weights_out=w_to)
+    assert L * 64 > 2 ** 32 and new.tolist() == [budget]
+    assert torch.equal(kept[0].long(), want)
+    assert torch.equal(to[0, :, :budget], rows) and torch.equal(w_to[0, :, :budget], totals)
+    assert not w_to[0, :, budget:].any()
+
+
 # ---------------------------------------------------------------- decodes
 
 
@@ -389,6 +414,22 @@ def test_probes_of_extreme_size(plx, G, d, scale, int4):
     for out in outs:
         err = np.abs(f64(out) - want) - allowed
         assert err.max() <= 0, err.max()
+
+
+def test_decode_with_weights_beyond_32_bit_offsets(plx):
+    """bf16 rows of the last head lie more than 2^32 bytes into their cache, its scores more than 2^31 into theirs."""
+    B, Hkv, G, L, d, n = 1, 2, 8, 36_000_000, 64, 500
+    c = random_case(70, B, Hkv, G, n, d)
+    K, V = (torch.empty((B, Hkv, L, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    K[:, :, :n], V[:, :, :n] = c["K"].cuda(), c["V"].cuda()
+    w = torch.zeros((B, Hkv, L), device="cuda")
+    w[:, :, :n] = c["w"].cuda()
+    sl = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = plx.decode_weights(c["q"].cuda(), c["r"].cuda(), K, V, sl, w)
+    args = f64(c["q"]), f64(c["r"]), f64(c["K"]), f64(c["V"]), [n]
+    check_out(out, *args)
+    check_weights(w[:, :, :n], *args, c["w"], c["w"])
+    assert not w[:, :, n:].any()
 
 
 def test_two_graphs_at_once_with_their_inputs_held(plx):
